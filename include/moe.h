@@ -23,6 +23,11 @@
  *                    combine
  *   moe_quantize_fp8, moe_expert_up_fp8, moe_expert_down_fp8, moe_forward_fp8
  *                    the layer with FP8 (E4M3) expert weights and activations
+ *   moe_quantize_fp8_block, moe_expert_up_fp8_block, moe_expert_down_fp8_block,
+ *   moe_forward_fp8_block
+ *                    the layer with FP8 experts scaled by blocks of 128
+ *   moe_balance_loss per-sequence balance and Z losses of a padded batch, expert
+ *                    counts, and the gradient of the logits
  *   moe_forward_train, moe_backward
  *                    training: the forward keeping its intermediates, and the
  *                    gradients of every input and weight
@@ -380,6 +385,100 @@ moe_status moe_expert_down_fp8(const moe_problem* p, const uint8_t* hq, const fl
 moe_status moe_forward_fp8(const moe_problem* p, const void* x, const void* Wg, const float* bg, const uint8_t* W1q,
                            const float* w1s, const uint8_t* W2q, const float* w2s, void* y, float* logits,
                            const moe_route_info* info, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------ FP8 experts, scales by block
+ * The FP8 layer above with finer scales (Skywork-MoE model card: an FP8
+ * checkpoint; Megatron-Core page, "关键特性": FP8): one for each block of 128
+ * values of K, so that a large value costs its own block the range and not
+ * its whole row, and h is quantised where it is computed, block by block.
+ *   activations: 1 x 128 blocks, E8M0 scales (a byte b stands for 2^(b-127)):
+ *     xq [T][d] codes, xs [T][d/128];  hq [T*k][F] codes, hs [T*k][F/128]
+ *   weights: 128 x 128 blocks, scales of type w_scale:
+ *     W1q [E][n1][d] codes, w1s [E][n1/128][d/128]  (gate rows first for SwiGLU)
+ *     W2q [E][d][F] codes,  w2s [E][d/128][F/128]
+ *     MOE_SCALE_E8M0: bytes; gfx950's matrix cores apply both scales of a block
+ *     themselves.  MOE_SCALE_F32: fp32 numbers, any finite value (a
+ *     checkpoint's own scales); each block's product is scaled in fp32.
+ * An E8M0 byte of 255 is NaN.  Requirements beyond the common limits:
+ * problem->dtype == MOE_BF16, d and F multiples of 128.  Codes must be 16-byte
+ * aligned, fp32 scales 4-byte, E8M0 scales need no alignment.  NaN and infinite
+ * values to quantise violate a precondition. */
+enum { MOE_SCALE_E8M0 = 0, MOE_SCALE_F32 = 1 };
+
+/* Quantise rows rows of K values (src_dtype MOE_F32 or MOE_BF16; K a multiple
+ * of 128) in blocks of block_rows x 128 (block_rows 1 or 128; a last block of
+ * fewer rows when rows is no multiple of 128).  Every block gets the smallest
+ * power of two s with max|block| <= 448 s, at least 2^-127 (s = 1 for an
+ * all-zero block), and the E4M3 codes nearest to v / s (ties to even): codes
+ * [rows][K], scales [ceil(rows/block_rows)][K/128] as E8M0 bytes or as the
+ * same numbers in fp32.  The weights of E experts are E*n1 (or E*d) rows.  No
+ * workspace. */
+moe_status moe_quantize_fp8_block(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t block_rows,
+                                  uint8_t* codes, void* scales, int32_t scale_type, void* stream);
+
+/* Bytes of workspace that suffice for every entry point below of this
+ * problem.  Host only. */
+moe_status moe_fp8_block_workspace_size(const moe_problem* p, size_t* bytes);
+
+/* First expert layer: u[r,n] = sum over blocks b of as[r,b] w1s[n/128,b] times
+ * the block's product of codes (fp32), for r in expert e's segment; h = max(u, 0)
+ * or silu(u_f) u_{F+f} in fp32, quantised in 1 x 128 blocks as
+ * moe_quantize_fp8_block does: hq [T*k][F], hs [T*k][F/128].  aq and as are
+ * those of x when src_token is given (rows gathered on the fly; T*d below
+ * 0xF0000000 bytes, else MOE_ERR_UNSUPPORTED), of the permuted rows when it is
+ * NULL.  Rows from offsets[E] on are left as they were.  offsets as in
+ * moe_expert_up.  ws (nullable; if given, ws_bytes >=
+ * moe_fp8_block_workspace_size) lets the last round of output tiles be split
+ * along K, its parts added in a fixed order. */
+moe_status moe_expert_up_fp8_block(const moe_problem* p, const uint8_t* aq, const uint8_t* as,
+                                   const int32_t* src_token, const int32_t* offsets, const uint8_t* W1q,
+                                   const void* w1s, int32_t w_scale, uint8_t* hq, uint8_t* hs, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Second expert layer: y_perm[r] = W2[e] h[r] from such codes, bf16 out.  Rows
+ * from offsets[E] on are left as they were.  ws as above. */
+moe_status moe_expert_down_fp8_block(const moe_problem* p, const uint8_t* hq, const uint8_t* hs,
+                                     const int32_t* offsets, const uint8_t* W2q, const void* w2s, int32_t w_scale,
+                                     void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* The whole layer: route and permute as moe_forward, quantise x per 1 x 128
+ * block, both expert layers on codes, combine.  Other arguments as
+ * moe_forward.  Needs ws_bytes >= moe_fp8_block_workspace_size; T*d >=
+ * 0xF0000000 returns MOE_ERR_UNSUPPORTED. */
+moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void* Wg, const float* bg,
+                                 const uint8_t* W1q, const void* w1s, const uint8_t* W2q, const void* w2s,
+                                 int32_t w_scale, void* y, float* logits, const moe_route_info* info, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------ balance loss of sequences
+ * moe_router_stats' auxiliary and Z losses (Megatron-Core page,
+ * "MoE负载均衡的挑战与应对" and "关键特性"; Skywork news, 技术创新 2) with the
+ * loads taken per sequence, and their gradient for a caller who has the logits
+ * (a gate of its own, trained outside moe_backward).
+ * Sequence s holds the n_s = seq_offsets[s+1] - seq_offsets[s] tokens from
+ * seq_offsets[s] on (device int32 [n_seq+1], non-decreasing, within [0, T];
+ * NULL: one sequence of all T tokens, n_seq == 1).  S+ sequences hold any
+ * token, N tokens lie in one:
+ *   counts[s,e] = number of (t,j) in s with topk_idx[t,j] == e  (entries
+ *                 outside [0,E) are skipped)           [n_seq][E] int32
+ *   aux = 1/S+ sum_s E sum_e counts[s,e]/(n_s k) (1/n_s) sum_t p[t,e]
+ *   Z   = 1/N sum_t (log sum_e exp logits[t,e])^2
+ *   losses [2] = {aux, Z} without their coefficients; {0, 0} when N == 0
+ *   dlogits [T][E] = gradient of aux_coef aux + z_coef Z with the counts
+ *                 constant: written for the tokens of a sequence; the rows of
+ *                 other tokens (padding) are left as they were.  NULL: none.
+ * p as in moe_route, after the optional normalisation (a token with equal
+ * logits then has no gradient from aux).  Without the normalisation a logit of
+ * -infinity (an expert closed to the token) has p = 0 and gradient 0, and a
+ * token whose logits are all -infinity adds nothing to either loss.  T == 0
+ * clears counts and losses.  Probabilities in fp32, sums over tokens in fp64 in
+ * fixed orders (the same bits on every run).  offsets outside [0, T] are
+ * clamped.  Uses T, E, k, normalize and lambda of the problem; 1 <= n_seq <=
+ * 2^20, n_seq * E < 2^31.  Needs ws_bytes >= moe_balance_workspace_size. */
+moe_status moe_balance_workspace_size(const moe_problem* p, int32_t n_seq, size_t* bytes);
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int32_t n_seq, float aux_coef, float z_coef, int32_t* counts,
+                            float* losses, float* dlogits, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,7 +10,10 @@ moe_route, moe_permute, moe_expert_up, moe_expert_down, moe_grouped_ffn,
 moe_combine, moe_forward, moe_router_stats, moe_shared_workspace_size,
 moe_shared_expert, moe_combine_shared, moe_quantize_fp8, moe_fp8_workspace_size,
 moe_expert_up_fp8, moe_expert_down_fp8, moe_forward_fp8, moe_forward_train,
-moe_backward_workspace_size, moe_backward, moe_forward_noalloc.
+moe_backward_workspace_size, moe_backward, moe_forward_noalloc,
+moe_quantize_fp8_block, moe_fp8_block_workspace_size, moe_expert_up_fp8_block,
+moe_expert_down_fp8_block, moe_forward_fp8_block, moe_balance_workspace_size,
+moe_balance_loss.
 """
 from __future__ import annotations
 
@@ -24,13 +27,16 @@ LIB_PATH = os.environ.get("MOE_LIB") or os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_ACT_RELU, MOE_ACT_SWIGLU = 0, 1
 MOE_F32, MOE_BF16 = 0, 1
+MOE_SCALE_E8M0, MOE_SCALE_F32 = 0, 1
 
 EXPORTS = ("moe_status_string", "moe_last_error", "moe_capacity", "moe_workspace_size", "moe_route",
            "moe_permute", "moe_expert_up", "moe_expert_down", "moe_grouped_ffn", "moe_combine", "moe_forward",
            "moe_router_stats", "moe_shared_workspace_size", "moe_shared_expert", "moe_combine_shared",
            "moe_quantize_fp8", "moe_fp8_workspace_size", "moe_expert_up_fp8", "moe_expert_down_fp8",
            "moe_forward_fp8", "moe_forward_train", "moe_backward_workspace_size", "moe_backward",
-           "moe_forward_noalloc")
+           "moe_forward_noalloc", "moe_quantize_fp8_block", "moe_fp8_block_workspace_size",
+           "moe_expert_up_fp8_block", "moe_expert_down_fp8_block", "moe_forward_fp8_block",
+           "moe_balance_workspace_size", "moe_balance_loss")
 
 
 class MoeError(RuntimeError):
@@ -101,6 +107,14 @@ def load() -> ctypes.CDLL:
     lib.moe_backward_workspace_size.argtypes = [PP, ctypes.POINTER(ctypes.c_size_t)]
     lib.moe_backward.argtypes = [PP, P, P, P, P, P, P, ctypes.POINTER(RouteInfo), ctypes.POINTER(Saved),
                                  ctypes.POINTER(RouterLosses), P, P, P, P, P, P, ctypes.c_size_t, P]
+    i32, size = ctypes.c_int32, ctypes.c_size_t
+    lib.moe_quantize_fp8_block.argtypes = [P, i32, ctypes.c_int64, i32, i32, P, P, i32, P]
+    lib.moe_fp8_block_workspace_size.argtypes = [PP, ctypes.POINTER(size)]
+    lib.moe_expert_up_fp8_block.argtypes = [PP, P, P, P, P, P, P, i32, P, P, P, size, P]
+    lib.moe_expert_down_fp8_block.argtypes = [PP, P, P, P, P, P, i32, P, P, size, P]
+    lib.moe_forward_fp8_block.argtypes = [PP, P, P, P, P, P, P, P, i32, P, P, ctypes.POINTER(RouteInfo), P, size, P]
+    lib.moe_balance_workspace_size.argtypes = [PP, i32, ctypes.POINTER(size)]
+    lib.moe_balance_loss.argtypes = [PP, P, P, P, i32, ctypes.c_float, ctypes.c_float, P, P, P, P, size, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = st
     _lib = lib
@@ -305,3 +319,79 @@ def moe_backward(p, dy, x, Wg, W1, W2, logits, info, saved, dx, dWg, dbg, dW1, d
                                ctypes.byref(sv) if sv is not None else None,
                                ctypes.byref(ls) if ls is not None else None, _ptr(dx), _ptr(dWg), _ptr(dbg),
                                _ptr(dW1), _ptr(dW2), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _scale_type(scales) -> int:
+    """MOE_SCALE_* of a tensor of block scales, by its element type."""
+    import torch
+    if scales.dtype == torch.float32:
+        return MOE_SCALE_F32
+    if scales.dtype in (torch.uint8, torch.float8_e8m0fnu):
+        return MOE_SCALE_E8M0
+    raise TypeError(f"block scales are float32 or E8M0 (uint8 or float8_e8m0fnu), not {scales.dtype}")
+
+
+def _e8m0(scales, name):
+    if scales is not None and not isinstance(scales, int) and _scale_type(scales) != MOE_SCALE_E8M0:
+        raise TypeError(f"{name}: activation scales are E8M0 (uint8 or float8_e8m0fnu), not {scales.dtype}")
+    return scales
+
+
+def moe_quantize_fp8_block(src, codes, scales, block_rows=1, stream=None):
+    """Rows of src (fp32 or bf16 tensor [rows, K]) to E4M3 codes (uint8 [rows, K])
+    with a power-of-two scale per block of block_rows (1 or 128) x 128 values;
+    scales [ceil(rows / block_rows), K / 128] is uint8 / float8_e8m0fnu (E8M0) or fp32."""
+    import torch
+    dt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}[src.dtype]
+    K = src.shape[-1]
+    rows = src.numel() // max(K, 1)
+    _check(load().moe_quantize_fp8_block(_ptr(src), dt, rows, K, int(block_rows), _ptr(codes), _ptr(scales),
+                                         _scale_type(scales), _stream(stream)))
+
+
+def moe_fp8_block_workspace_size(p) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_fp8_block_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def moe_expert_up_fp8_block(p, aq, a_scale, src_token, offsets, W1q, w1s, hq, hs, ws=None, stream=None):
+    """aq, a_scale: codes and E8M0 scales of x (rows gathered through src_token) or
+    of the permuted rows (src_token None); w1s: E8M0 or fp32 scales; hq, hs: out."""
+    _check(load().moe_expert_up_fp8_block(ctypes.byref(p), _ptr(aq), _ptr(_e8m0(a_scale, "a_scale")),
+                                          _ptr(src_token), _ptr(offsets), _ptr(W1q), _ptr(w1s), _scale_type(w1s),
+                                          _ptr(hq), _ptr(_e8m0(hs, "hs")), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_expert_down_fp8_block(p, hq, hs, offsets, W2q, w2s, y_perm, ws=None, stream=None):
+    _check(load().moe_expert_down_fp8_block(ctypes.byref(p), _ptr(hq), _ptr(_e8m0(hs, "hs")), _ptr(offsets),
+                                            _ptr(W2q), _ptr(w2s), _scale_type(w2s), _ptr(y_perm), _ptr(ws),
+                                            _nbytes(ws), _stream(stream)))
+
+
+def moe_forward_fp8_block(p, x, Wg, bg, W1q, w1s, W2q, w2s, y, logits=None, info=None, ws=None, stream=None):
+    """The layer with block-scaled FP8 experts; w1s and w2s of one type (E8M0 or fp32)."""
+    kind = _scale_type(w1s)
+    if _scale_type(w2s) != kind:
+        raise TypeError("w1s and w2s must be scales of one type")
+    ri = _route_info(info) if info else None
+    _check(load().moe_forward_fp8_block(ctypes.byref(p), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1q), _ptr(w1s),
+                                        _ptr(W2q), _ptr(w2s), kind, _ptr(y), _ptr(logits),
+                                        ctypes.byref(ri) if ri is not None else None, _ptr(ws), _nbytes(ws),
+                                        _stream(stream)))
+
+
+def moe_balance_workspace_size(p, n_seq) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_balance_workspace_size(ctypes.byref(p), int(n_seq), ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(p, logits, topk_idx, seq_offsets, counts, losses, dlogits, aux_coef=0.0, z_coef=0.0, ws=None,
+                     stream=None):
+    """counts [n_seq, E] int32, losses [2] = (aux, Z), dlogits [T, E] (or None) of
+    the sequences seq_offsets [n_seq + 1] int32 (None: one sequence of all tokens)."""
+    n_seq = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    _check(load().moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
+                                   float(aux_coef), float(z_coef), _ptr(counts), _ptr(losses), _ptr(dlogits),
+                                   _ptr(ws), _nbytes(ws), _stream(stream)))

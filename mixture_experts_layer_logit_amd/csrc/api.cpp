@@ -59,6 +59,17 @@ hipError_t moe_launch_grouped_gemm_fp8(int epi, const void* A, const int32_t* ga
                                        void* C, const int32_t* offsets, int E, int K, int Nw, int Nout, int F,
                                        int max_rows, int mean_rows, int ncu, float* partial, const float* a_scale,
                                        const float* w_scale, hipStream_t stream);
+hipError_t moe_launch_quantize_block(int dtype, const void* src, long long R, int K, int block_rows, int f32,
+                                     uint8_t* codes, void* scales, hipStream_t stream);
+size_t moe_block_gemm_partial_bytes(int mean_rows);
+hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint8_t* As, const int32_t* gather,
+                                 int gather_rows, const uint8_t* W, const void* Ws, uint8_t* Hq, uint8_t* Hs, void* Y,
+                                 const int32_t* offsets, int E, int K, int Nw, int Nout, int F, int max_rows,
+                                 int mean_rows, int ncu, float* partial, hipStream_t stream);
+size_t moe_balance_scratch_bytes(int T, int S);
+hipError_t moe_launch_balance(const float* logits, const int32_t* topk_idx, const int32_t* offsets, int S, int T,
+                              int E, int k, int normalize, float lambda, float aux_coef, float z_coef,
+                              int32_t* counts, float* losses, float* dlogits, void* scratch, hipStream_t stream);
 hipError_t moe_launch_router_stats(const float* logits, int T, int E, int k, int normalize, float lambda,
                                    const int32_t* counts, const int32_t* offsets, double* partial, float* frac,
                                    float* mean_prob, float* scalars, hipStream_t stream);
@@ -71,6 +82,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 8;
 constexpr int kMaxT = 1 << 24;
 constexpr int kMaxDim = 65536;
+constexpr int kMaxSeq = 1 << 20;  // sequences of a balance loss
 constexpr size_t kAlign = 256;
 // The fused row gather of the up projection addresses x with 32-bit byte
 // offsets, and offsets from 0xF0000000 up are its out-of-range marker.
@@ -436,6 +448,92 @@ moe_status do_down_fp8(const moe_problem* p, const void* hq, const float* hs, co
                                                   p->F, p->T * p->k, mean_rows_of(p), cu_count(), partial, hs, w2s,
                                                   s),
                       "FP8 expert down launch");
+}
+
+moe_status check_balance(const moe_problem* p, int32_t n_seq)
+{
+    CHECK(check_problem(p));
+    if (n_seq < 1)
+        return fail(MOE_ERR_INVALID_ARG, "n_seq=%d is below 1", n_seq);
+    if (n_seq > kMaxSeq || (long long)n_seq * p->E > INT32_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "n_seq=%d above %d, or n_seq * E above 2^31 - 1", n_seq, kMaxSeq);
+    return MOE_OK;
+}
+
+// ---- FP8 experts with scales by block
+struct LayoutFp8Block {
+    size_t topk_idx, topk_w, counts, offsets, slot, src_token, chunk_cnt, logits, partial, xq, xs, hq, hs, y_perm,
+        total;
+};
+
+LayoutFp8Block layout_fp8_block_of(const moe_problem* p)
+{
+    LayoutFp8Block L;
+    const size_t T = (size_t)p->T, k = (size_t)p->k, E = (size_t)p->E, d = (size_t)p->d, F = (size_t)p->F;
+    const size_t nchunks = (T + kChunk - 1) / kChunk;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round_up(bytes);
+        return at;
+    };
+    L.topk_idx = take(T * k * 4);
+    L.topk_w = take(T * k * 4);
+    L.counts = take(E * 4);
+    L.offsets = take((E + 1) * 4);
+    L.slot = take(T * k * 4);
+    L.src_token = take(T * k * 4);
+    L.chunk_cnt = take(std::max<size_t>(nchunks, 1) * E * 4);
+    L.logits = take(T * E * 4);
+    L.partial = take(moe_block_gemm_partial_bytes(mean_rows_of(p)));
+    L.xq = take(T * d);
+    L.xs = take(T * (d / 128));
+    L.hq = take(T * k * F);
+    L.hs = take(T * k * (F / 128));
+    L.y_perm = take(T * k * d * 2);
+    L.total = off;
+    return L;
+}
+
+moe_status check_ws_fp8_block(const moe_problem* p, const void* ws, size_t ws_bytes)
+{
+    const size_t need = layout_fp8_block_of(p).total;
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+    return check_ptr(ws, "ws", 16);
+}
+
+moe_status check_scale_type(int32_t type, const char* name)
+{
+    if (type != MOE_SCALE_E8M0 && type != MOE_SCALE_F32)
+        return fail(MOE_ERR_INVALID_ARG, "%s=%d is neither MOE_SCALE_E8M0 nor MOE_SCALE_F32", name, type);
+    return MOE_OK;
+}
+
+moe_status check_scales(const void* scales, int32_t type, const char* name)
+{
+    return check_ptr(scales, name, type == MOE_SCALE_F32 ? 4 : 1);
+}
+
+moe_status do_up_fp8_block(const moe_problem* p, const uint8_t* aq, const uint8_t* as, const int32_t* gather,
+                           const int32_t* offsets, const uint8_t* W1q, const void* w1s, int32_t w_scale, uint8_t* hq,
+                           uint8_t* hs, float* partial, hipStream_t s)
+{
+    const int epi = p->act == MOE_ACT_SWIGLU ? 2 : 1;
+    return hip_status(moe_launch_block_gemm(epi, w_scale == MOE_SCALE_F32, aq, as, gather, p->T, W1q, w1s, hq, hs,
+                                            nullptr, offsets, p->E, p->d, n1_of(p), p->F, p->F, p->T * p->k,
+                                            mean_rows_of(p), cu_count(), partial, s),
+                      "block FP8 expert up launch");
+}
+
+moe_status do_down_fp8_block(const moe_problem* p, const uint8_t* hq, const uint8_t* hs, const int32_t* offsets,
+                             const uint8_t* W2q, const void* w2s, int32_t w_scale, void* y_perm, float* partial,
+                             hipStream_t s)
+{
+    return hip_status(moe_launch_block_gemm(0, w_scale == MOE_SCALE_F32, hq, hs, nullptr, 0, W2q, w2s, nullptr,
+                                            nullptr, y_perm, offsets, p->E, p->F, p->d, p->d, p->F, p->T * p->k,
+                                            mean_rows_of(p), cu_count(), partial, s),
+                      "block FP8 expert down launch");
 }
 
 // ---- backward
@@ -957,6 +1055,179 @@ moe_status moe_forward_fp8(const moe_problem* p, const void* x, const void* Wg, 
                      "FP8 quantisation launch"));
     CHECK(do_down_fp8(p, hq, hs, offsets, W2q, w2s, y_perm, partial, s));
     CHECK(do_combine(p, y_perm, slot, topk_w, nullptr, y, s));
+    return ok();
+}
+
+moe_status moe_quantize_fp8_block(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t block_rows,
+                                  uint8_t* codes, void* scales, int32_t scale_type, void* stream)
+{
+    if (src_dtype != MOE_F32 && src_dtype != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "src_dtype=%d is neither MOE_F32 nor MOE_BF16", src_dtype);
+    CHECK(check_scale_type(scale_type, "scale_type"));
+    if (block_rows != 1 && block_rows != 128)
+        return fail(MOE_ERR_INVALID_ARG, "block_rows=%d is neither 1 nor 128", block_rows);
+    if (rows < 0)
+        return fail(MOE_ERR_INVALID_ARG, "rows=%lld is negative", (long long)rows);
+    if (K < 128 || K > kMaxDim || K % 128)
+        return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 128 in [128, %d]", K, kMaxDim);
+    if (rows > ((long long)1 << 40) / K || rows > INT32_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "too many rows");
+    if (rows == 0)
+        return ok();
+    CHECK(check_ptr(src, "src", 16));
+    CHECK(check_ptr(codes, "codes", 16));
+    CHECK(check_scales(scales, scale_type, "scales"));
+    CHECK(hip_status(moe_launch_quantize_block(src_dtype == MOE_F32 ? 0 : 1, src, rows, K, block_rows,
+                                               scale_type == MOE_SCALE_F32, codes, scales, (hipStream_t)stream),
+                     "block FP8 quantisation launch"));
+    return ok();
+}
+
+moe_status moe_fp8_block_workspace_size(const moe_problem* p, size_t* bytes)
+{
+    CHECK(check_fp8(p));
+    if (!bytes)
+        return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = layout_fp8_block_of(p).total;
+    return ok();
+}
+
+moe_status moe_expert_up_fp8_block(const moe_problem* p, const uint8_t* aq, const uint8_t* as,
+                                   const int32_t* src_token, const int32_t* offsets, const uint8_t* W1q,
+                                   const void* w1s, int32_t w_scale, uint8_t* hq, uint8_t* hs, void* ws,
+                                   size_t ws_bytes, void* stream)
+{
+    CHECK(check_fp8(p));
+    CHECK(check_scale_type(w_scale, "w_scale"));
+    if (p->T == 0)
+        return ok();
+    CHECK(check_ptr(aq, src_token ? "xq" : "x_perm codes", 16));
+    CHECK(check_ptr(as, "activation scales", 1));
+    if (src_token) {
+        CHECK(check_ptr(src_token, "src_token", 4));
+        if (!gather_ok_fp8(p))
+            return fail(MOE_ERR_UNSUPPORTED, "x codes of %llu bytes are too large to gather; pass permuted codes",
+                        (unsigned long long)p->T * p->d);
+    }
+    CHECK(check_ptr(offsets, "offsets", 4));
+    CHECK(check_ptr(W1q, "W1q", 16));
+    CHECK(check_scales(w1s, w_scale, "w1s"));
+    CHECK(check_ptr(hq, "hq", 16));
+    CHECK(check_ptr(hs, "hs", 1));
+    if (ws)
+        CHECK(check_ws_fp8_block(p, ws, ws_bytes));
+    float* partial = ws ? at<float>(ws, layout_fp8_block_of(p).partial) : nullptr;
+    CHECK(do_up_fp8_block(p, aq, as, src_token, offsets, W1q, w1s, w_scale, hq, hs, partial, (hipStream_t)stream));
+    return ok();
+}
+
+moe_status moe_expert_down_fp8_block(const moe_problem* p, const uint8_t* hq, const uint8_t* hs,
+                                     const int32_t* offsets, const uint8_t* W2q, const void* w2s, int32_t w_scale,
+                                     void* y_perm, void* ws, size_t ws_bytes, void* stream)
+{
+    CHECK(check_fp8(p));
+    CHECK(check_scale_type(w_scale, "w_scale"));
+    if (p->T == 0)
+        return ok();
+    CHECK(check_ptr(hq, "hq", 16));
+    CHECK(check_ptr(hs, "hs", 1));
+    CHECK(check_ptr(offsets, "offsets", 4));
+    CHECK(check_ptr(W2q, "W2q", 16));
+    CHECK(check_scales(w2s, w_scale, "w2s"));
+    CHECK(check_ptr(y_perm, "y_perm", 16));
+    if (ws)
+        CHECK(check_ws_fp8_block(p, ws, ws_bytes));
+    float* partial = ws ? at<float>(ws, layout_fp8_block_of(p).partial) : nullptr;
+    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, partial, (hipStream_t)stream));
+    return ok();
+}
+
+moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void* Wg, const float* bg,
+                                 const uint8_t* W1q, const void* w1s, const uint8_t* W2q, const void* w2s,
+                                 int32_t w_scale, void* y, float* logits, const moe_route_info* info, void* ws,
+                                 size_t ws_bytes, void* stream)
+{
+    CHECK(check_fp8(p));
+    CHECK(check_scale_type(w_scale, "w_scale"));
+    if (p->T == 0)
+        return ok();
+    if (!gather_ok_fp8(p))
+        return fail(MOE_ERR_UNSUPPORTED, "x codes of %llu bytes are too large to gather (limit 0xF0000000 bytes)",
+                    (unsigned long long)p->T * p->d);
+    CHECK(check_ptr(w1s, "w1s", w_scale == MOE_SCALE_F32 ? 4 : 1));
+    CHECK(check_ptr(w2s, "w2s", w_scale == MOE_SCALE_F32 ? 4 : 1));
+    CHECK(check_forward(p, x, Wg, bg, W1q, W2q, y, logits));
+    CHECK(check_ws_fp8_block(p, ws, ws_bytes));
+    const LayoutFp8Block L = layout_fp8_block_of(p);
+    moe_route_info r = {};
+    if (info)
+        r = *info;
+#define PICK(field, type) (r.field ? r.field : at<type>(ws, L.field))
+    int32_t* topk_idx = PICK(topk_idx, int32_t);
+    float* topk_w = PICK(topk_w, float);
+    int32_t* counts = PICK(counts, int32_t);
+    int32_t* offsets = PICK(offsets, int32_t);
+    int32_t* slot = PICK(slot, int32_t);
+    int32_t* src_token = PICK(src_token, int32_t);
+#undef PICK
+    const void* ptrs[] = {topk_idx, topk_w, counts, offsets, slot, src_token};
+    for (const void* q : ptrs)
+        CHECK(check_ptr(q, "route info field", 4));
+    float* z = logits ? logits : at<float>(ws, L.logits);
+    float* partial = at<float>(ws, L.partial);
+    uint8_t* xq = at<uint8_t>(ws, L.xq);
+    uint8_t* xs = at<uint8_t>(ws, L.xs);
+    uint8_t* hq = at<uint8_t>(ws, L.hq);
+    uint8_t* hs = at<uint8_t>(ws, L.hs);
+    void* y_perm = at<char>(ws, L.y_perm);
+    hipStream_t s = (hipStream_t)stream;
+    CHECK(do_route(p, Wg ? x : nullptr, Wg, bg, z, topk_idx, topk_w, s));
+    CHECK(hip_status(moe_launch_permute(p->dtype, topk_idx, x, p->T, p->d, p->E, p->k, capacity_of(p), counts,
+                                        offsets, slot, src_token, nullptr, at<int32_t>(ws, L.chunk_cnt), s),
+                     "permute launch"));
+    CHECK(hip_status(moe_launch_quantize_block(1, x, p->T, p->d, 1, 0, xq, xs, s), "block FP8 quantisation launch"));
+    CHECK(do_up_fp8_block(p, xq, xs, src_token, offsets, W1q, w1s, w_scale, hq, hs, partial, s));
+    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, partial, s));
+    CHECK(do_combine(p, y_perm, slot, topk_w, nullptr, y, s));
+    return ok();
+}
+
+moe_status moe_balance_workspace_size(const moe_problem* p, int32_t n_seq, size_t* bytes)
+{
+    CHECK(check_balance(p, n_seq));
+    if (!bytes)
+        return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = round_up(moe_balance_scratch_bytes(p->T, n_seq));
+    return ok();
+}
+
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int32_t n_seq, float aux_coef, float z_coef, int32_t* counts,
+                            float* losses, float* dlogits, void* ws, size_t ws_bytes, void* stream)
+{
+    CHECK(check_balance(p, n_seq));
+    if (seq_offsets)
+        CHECK(check_ptr(seq_offsets, "seq_offsets", 4));
+    else if (n_seq != 1)
+        return fail(MOE_ERR_INVALID_ARG, "n_seq=%d sequences without seq_offsets", n_seq);
+    if (!std::isfinite(aux_coef) || !std::isfinite(z_coef))
+        return fail(MOE_ERR_INVALID_ARG, "balancing-loss coefficients must be finite");
+    CHECK(check_ptr(counts, "counts", 4));
+    CHECK(check_ptr(losses, "losses", 4));
+    if (p->T > 0) {
+        CHECK(check_ptr(logits, "logits", 4));
+        CHECK(check_ptr(topk_idx, "topk_idx", 4));
+        if (dlogits)
+            CHECK(check_ptr(dlogits, "dlogits", 4));
+    }
+    const size_t need = round_up(moe_balance_scratch_bytes(p->T, n_seq));
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+    CHECK(check_ptr(ws, "ws", 16));
+    CHECK(hip_status(moe_launch_balance(logits, topk_idx, seq_offsets, n_seq, p->T, p->E, p->k, p->normalize,
+                                        p->lambda, aux_coef, z_coef, counts, losses, dlogits, ws,
+                                        (hipStream_t)stream),
+                     "balance loss launch"));
     return ok();
 }
 

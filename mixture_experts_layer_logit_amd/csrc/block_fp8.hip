@@ -1,0 +1,611 @@
+// Block-scaled FP8 experts (gfx950): quantisation to E4M3 codes with a scale
+// for each block of 128 values, and the grouped GEMMs of the two expert
+// layers on such codes.
+//
+// FP8 experts (Skywork-MoE model card: an FP8 checkpoint; news item
+// "4090推理": FP8-quantised inference; Megatron-Core page, "关键特性": FP8
+// among the coming features).  Activations carry one scale per 1 x 128 block
+// of a row, weights one per 128 x 128 block of a matrix:
+//   u[r, n] = sum_b sA[r, b] sW[n / 128, b] sum_{k in block b} a[r, k] w[n, k]
+// Activation scales are E8M0 bytes (b stands for 2^(b - 127)); weight scales
+// are E8M0 bytes or fp32 numbers.
+#include <algorithm>
+
+#include "common.h"
+#include "fp8.h"
+#include "gemm_common.h"
+
+namespace moe {
+
+constexpr int kBlk = 128;  // values of K that share a scale, and rows of a weight block
+
+// ---------------------------------------------------------------- quantisation
+// Each block gets the smallest power-of-two scale s with max|block| <= 448 s,
+// at least 2^-127 (s = 1 for an all-zero block), and each value the E4M3 code
+// nearest to v / s (ties to even); v / s is exact, so every code is decided
+// exactly.
+
+// One scale as the E8M0 byte or the fp32 number.
+template <bool F32>
+__device__ __forceinline__ void store_scale(void* scales, size_t i, int e)
+{
+    if constexpr (F32)
+        static_cast<float*>(scales)[i] = ldexpf(1.0f, e);
+    else
+        static_cast<uint8_t*>(scales)[i] = (uint8_t)(e + 127);
+}
+
+// 1 x 128 blocks: 16 lanes of 8 values each per block, the blocks of all rows
+// in one run (K is a multiple of 128).
+template <typename ET, bool F32>
+__global__ __launch_bounds__(256) void moe_quantize_rows_kernel(const typename ET::storage* __restrict__ src,
+                                                                long long blocks, uint8_t* __restrict__ codes,
+                                                                void* __restrict__ scales)
+{
+    const long long b = (long long)blockIdx.x * 16 + threadIdx.x / 16;
+    if (b >= blocks)
+        return;
+    const size_t at = (size_t)b * kBlk + 8 * (threadIdx.x % 16);
+    float f[8], amax = 0.0f;
+    load8(src + at, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor(amax, o));
+    const int e = fp8_block_scale_exp(amax);
+    *reinterpret_cast<uint2*>(codes + at) = e4m3_encode8(f, e);
+    if (threadIdx.x % 16 == 0)
+        store_scale<F32>(scales, (size_t)b, e);
+}
+
+// 128 x 128 blocks, one per workgroup (the last block row may be shorter):
+// thread t takes 8 columns of rows t / 16, t / 16 + 16, ..., held in registers
+// between the maximum and the codes.
+template <typename ET, bool F32>
+__global__ __launch_bounds__(256) void moe_quantize_tiles_kernel(const typename ET::storage* __restrict__ src,
+                                                                 long long R, int K, uint8_t* __restrict__ codes,
+                                                                 void* __restrict__ scales)
+{
+    __shared__ float s_max[4];
+    const int nkb = K / kBlk;
+    const long long br = blockIdx.x / nkb;
+    const int bc = blockIdx.x % nkb;
+    const long long r0 = br * kBlk;
+    const size_t col = (size_t)bc * kBlk + 8 * (threadIdx.x % 16);
+    float f[8][8], amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long long r = r0 + threadIdx.x / 16 + 16 * i;
+        load8(src + (size_t)min(r, R - 1) * K + col, f[i]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            amax = fmaxf(amax, r < R ? fabsf(f[i][q]) : 0.0f);
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor(amax, o));
+    if (lane_id() == 0)
+        s_max[threadIdx.x / kWave] = amax;
+    __syncthreads();
+    amax = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const int e = fp8_block_scale_exp(amax);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long long r = r0 + threadIdx.x / 16 + 16 * i;
+        if (r < R)
+            *reinterpret_cast<uint2*>(codes + (size_t)r * K + col) = e4m3_encode8(f[i], e);
+    }
+    if (threadIdx.x == 0)
+        store_scale<F32>(scales, (size_t)blockIdx.x, e);
+}
+
+// ---------------------------------------------------------------- grouped GEMM
+// Rows of expert e's segment times its weight matrix.  Block tile BM x 256,
+// WM x WN wavefronts, K in slices of 128 values (one scale block), each slice
+// loaded from memory straight into one of S LDS stages.  The 256 weight rows
+// of a tile are two halves of 128: for SwiGLU the gate rows and the matching
+// up rows of 128 hidden columns, else 256 consecutive rows; each half lies in
+// one row of weight blocks, so a tile has two weight scales per slice.  A
+// wavefront takes the same rows of both halves, so the gate and up values of
+// a hidden column meet in one lane.
+//
+// MFMA 32x32x64 f8f6f4 with block scales: lane l holds 32 consecutive K
+// values of operand row l % 32 (the half l / 32 of the 64) and the E8M0 byte
+// that scales them, so the matrix core applies both scales of a block to the
+// products itself.  The weight tile is its first operand, the activation tile
+// its second: a lane's accumulators are 4 consecutive columns of one row.
+enum { BEPI_NONE = 0, BEPI_RELU = 1, BEPI_SWIGLU = 2 };
+
+constexpr int kBlkMaxParts = 16;     // K parts of a tail tile
+constexpr int kBlkSplitSlots = 256;  // partial tiles the workspace holds
+constexpr int kBlkMinPart = 4;       // K slices of a part
+[[maybe_unused]] constexpr int kBlkMaxSlices = 512;   // K <= 65536
+
+template <int BM_, int WM_, int WN_, int S_, int GM_>
+struct BlockShape {
+    static constexpr int BM = BM_, BN = 256, WM = WM_, WN = WN_, S = S_, GM = GM_, RB = 128;
+    static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
+    static constexpr int kWavesPerSimd = kWaves / 4;
+    static constexpr int kWaveM = BM / WM, kWaveN = BN / WN;
+    static constexpr int kFM = kWaveM / 32, kFN = kWaveN / 32;
+    static constexpr int kLdsA = BM * RB, kLdsW = BN * RB;
+    static constexpr int kScl = kThreads * 4;  // scales of the slice's activation rows, a dword each
+    static constexpr int kStage = kLdsA + kLdsW + kScl;
+    static constexpr int kBlkA = BM / 8 / kWaves, kBlkW = BN / 8 / kWaves;  // 1 KB loads per wavefront and slice
+    static constexpr int kLoads = kBlkA + kBlkW + 1;
+    static constexpr int kTileFloats = BM * BN;
+    static_assert(kFN % 2 == 0, "a wavefront takes rows of both weight halves");
+    static_assert(kWaves % 4 == 0 && BM % (8 * kWaves) == 0 && kThreads >= BM, "loads split evenly");
+    static_assert((S - 1) * kLoads <= 63, "vmcnt range");
+    static_assert(2 * (WM * 32) * BN * 4 <= S * kStage, "two staged row fragments fit the stages");
+};
+
+struct BlockGemmArgs {
+    const uint8_t* A;       // codes of the activation rows [.][K]
+    const uint8_t* As;      // their scales [.][K / 128]
+    const int32_t* gather;  // nullable: row r is A's row gather[r] of gather_rows
+    int gather_rows;
+    const uint8_t* W;  // [E][Nw][K]
+    const void* Ws;    // [E][Nw / 128][K / 128]
+    uint8_t* Hq;       // codes of the hidden rows [.][Nout] (activation epilogues)
+    uint8_t* Hs;       // their scales [.][Nout / 128]
+    uint16_t* Y;       // bf16 rows [.][Nout] (plain epilogue)
+    const int32_t* offsets;
+    int E, K, Nw, Nout, F, max_rows;
+    float* partial;  // nullable: no K split
+};
+
+template <typename S>
+__device__ __forceinline__ uint32_t bswz(int row, int c)
+{
+    return row * S::RB + ((c ^ ((row >> 1) & 7)) << 4);
+}
+
+// One dword per lane from a byte of buffer `rsrc` at voff + soff, zero
+// extended, into LDS at byte address lds + 4 * lane (see dma16).
+__device__ __forceinline__ void dma_byte(const i32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff)
+{
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
+    uint32_t so = __builtin_amdgcn_readfirstlane(soff);
+    __asm__("" : "+s"(so));
+    __asm__ volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                     :
+                     : "s"(m0), "v"(voff), "s"(rsrc), "s"(so)
+                     : "memory");
+}
+
+__device__ __forceinline__ int block_parts(int total, int G, int nk, bool enabled)
+{
+    const int tail = total % G;
+    if (!enabled || tail == 0)
+        return 1;
+    return max(1, min(min(kBlkMaxParts, min(G, kBlkSplitSlots) / tail), nk / kBlkMinPart));
+}
+
+// Epilogue of row fragment i of every wavefront (WM bands of 32 rows), whose
+// accumulators are acc[0 .. kFN): staged in LDS as [band row][column] (16-byte
+// chunks XOR-swizzled by the row), then taken row by row.  Activation
+// epilogues: fp32 h is quantised as it is, without a rounding to bf16 in
+// between, block by block; a block's 128 values are spread over a few lanes of
+// one wavefront.
+template <typename S, int EPI>
+__device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, const TileDec& t, uint8_t* buf,
+                                            const BlockGemmArgs& g)
+{
+    constexpr bool kGlu = EPI == BEPI_SWIGLU;
+    constexpr int HC = kGlu ? 128 : 256;  // output columns of the tile
+    constexpr int kRows = S::WM * 32;
+    constexpr int kEl = EPI == BEPI_NONE ? 2 : 4;
+    constexpr int kRowBytes = HC * kEl;
+    constexpr int kSwz = kRowBytes / 16 - 1 < 31 ? kRowBytes / 16 - 1 : 31;
+    int tid = threadIdx.x;
+    __asm__ volatile("" : "+v"(tid));
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int r = wm * 32 + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < (kGlu ? S::kFN / 2 : S::kFN); ++j)
+#pragma unroll
+        for (int g4 = 0; g4 < 4; ++g4) {
+            constexpr int kHalfN = S::kWaveN / 2, kHalfF = S::kFN / 2;
+            const int col = (j / kHalfF) * 128 + wn * kHalfN + (j % kHalfF) * 32 + 8 * g4 + 4 * (lane >> 5);
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float u = acc[j][4 * g4 + q];
+                if constexpr (kGlu)
+                    v[q] = u / (1.0f + __expf(-u)) * acc[j + kHalfF][4 * g4 + q];
+                else if constexpr (EPI == BEPI_RELU)
+                    v[q] = fmaxf(u, 0.0f);
+                else
+                    v[q] = u;
+            }
+            const int byte = col * kEl;
+            uint8_t* dst = buf + r * kRowBytes + (((byte >> 4) ^ (r & kSwz)) << 4) + (byte & 15);
+            if constexpr (kEl == 2) {
+                uint2 o;
+                o.x = f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16);
+                o.y = f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16);
+                *reinterpret_cast<uint2*>(dst) = o;
+            } else {
+                *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    lds_barrier();
+    if constexpr (EPI == BEPI_NONE) {
+        constexpr int kChunks = kRowBytes / 16;
+#pragma unroll
+        for (int it = 0; it < kRows * kChunks / S::kThreads; ++it) {
+            const int c = tid + it * S::kThreads;
+            const int rr = c / kChunks, q = c % kChunks;
+            const int m = (rr / 32) * S::kWaveM + i * 32 + (rr % 32);
+            if (m < t.rows && t.n0 + q * 8 < g.Nout)
+                *reinterpret_cast<uint4*>(g.Y + (size_t)(t.row0 + m) * g.Nout + t.n0 + q * 8) =
+                    *reinterpret_cast<const uint4*>(buf + rr * kRowBytes + ((q ^ (rr & kSwz)) << 4));
+        }
+    } else {
+        constexpr int kPer = S::kThreads / kRows;  // threads of a row
+        constexpr int V = HC / kPer;               // consecutive values of a thread
+        constexpr int kLanes = kBlk / V;           // lanes of a block
+        const int rr = tid / kPer, part = tid % kPer;
+        const int m = (rr / 32) * S::kWaveM + i * 32 + (rr % 32);
+        const int n = t.n0 + part * V;
+        float f[V], amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+            const int q = part * (V / 4) + c;
+            const float4 x = *reinterpret_cast<const float4*>(buf + rr * kRowBytes + ((q ^ (rr & kSwz)) << 4));
+            f[4 * c] = x.x;
+            f[4 * c + 1] = x.y;
+            f[4 * c + 2] = x.z;
+            f[4 * c + 3] = x.w;
+            amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor(amax, o));
+        const int e = fp8_block_scale_exp(amax);
+        if (m < t.rows && n < g.Nout) {
+            uint8_t* out = g.Hq + (size_t)(t.row0 + m) * g.Nout + n;
+#pragma unroll
+            for (int c = 0; c < V / 16; ++c) {
+                const uint2 lo = e4m3_encode8(f + 16 * c, e), hi = e4m3_encode8(f + 16 * c + 8, e);
+                *reinterpret_cast<uint4*>(out + 16 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+            if (part % kLanes == 0)
+                g.Hs[(size_t)(t.row0 + m) * (g.Nout / kBlk) + n / kBlk] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+template <typename S, int EPI, bool WF32>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
+void moe_block_gemm_kernel(BlockGemmArgs g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)  // the body uses device-only types; the host pass needs the stub only
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
+    __shared__ uint32_t s_ws[2][kBlkMaxSlices];  // the tile's weight scales
+    __shared__ int32_t s_pref[kGemmMaxE + 1];
+    __shared__ int32_t s_wsum[S::kWaves];
+    const int tid = threadIdx.x;
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int K = g.K, nk = K / kBlk;
+    const uint32_t lds0 = lds_addr(lds);
+    constexpr int kHalfN = S::kWaveN / 2, kHalfF = S::kFN / 2;
+
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
+    const int total = s_pref[g.E];
+    const int G = gridDim.x;
+    const int parts = block_parts(total, G, nk, g.partial != nullptr);
+    const int full = parts > 1 ? total - total % G : total;
+    const int tail = total - full;
+    const int items = full + tail * parts;
+
+    for (int base = 0; base < items; base += G) {
+        const int b = blockIdx.x;
+        const int item = (G % 8 == 0) ? base + (b % 8) * (G / 8) + b / 8 : base + b;  // an XCD's blocks side by side
+        if (item >= items)
+            continue;
+        int tile = item, k0 = 0, k1 = nk, slot = -1;
+        if (item >= full) {
+            const int j = item - full, part = j / tail;
+            tile = full + j % tail;
+            k0 = part * nk / parts;
+            k1 = (part + 1) * nk / parts;
+            slot = (j % tail) * parts + part;
+        }
+        const TileDec t = decode_tile<S>(tile, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
+
+        // lane's place in a 1 KB load of 8 rows: row lane / 8, physical chunk
+        // lane % 8; a wavefront's loads all have the parity of its number
+        const int lrow = lane / 8;
+        const int lchunk = (lane % 8) ^ ((((wave & 1) << 2) + (lrow >> 1)) & 7);
+        i32x4 rsA, rsS;
+        uint32_t voffA[S::kBlkA], voffS;
+        const int srow = wave * kWave + lane;  // the tile row whose scale this lane loads
+        if (g.gather) {
+            rsA = make_rsrc(g.A, (uint32_t)g.gather_rows * (uint32_t)K);
+            rsS = make_rsrc(g.As, (uint32_t)g.gather_rows * (uint32_t)nk);
+#pragma unroll
+            for (int i = 0; i < S::kBlkA; ++i) {
+                const int r = 8 * (wave + S::kWaves * i) + lrow;
+                const int src = r < t.rows ? g.gather[t.row0 + r] : -1;
+                voffA[i] = src >= 0 && src < g.gather_rows ? (uint32_t)src * (uint32_t)K + lchunk * 16 : 0xf0000000u;
+            }
+            const int src = srow < t.rows ? g.gather[t.row0 + srow] : -1;
+            voffS = src >= 0 && src < g.gather_rows ? (uint32_t)src * (uint32_t)nk : 0xf0000000u;
+        } else {
+            rsA = make_rsrc(g.A + (size_t)t.row0 * K, (uint32_t)t.rows * (uint32_t)K);
+            rsS = make_rsrc(g.As + (size_t)t.row0 * nk, (uint32_t)t.rows * (uint32_t)nk);
+#pragma unroll
+            for (int i = 0; i < S::kBlkA; ++i)
+                voffA[i] = (uint32_t)(8 * (wave + S::kWaves * i) + lrow) * (uint32_t)K + lchunk * 16;
+            voffS = srow < t.rows ? (uint32_t)srow * (uint32_t)nk : 0xf0000000u;
+        }
+        const i32x4 rsW = make_rsrc(g.W + (size_t)t.e * g.Nw * K, (uint32_t)g.Nw * (uint32_t)K);
+        uint32_t voffW[S::kBlkW];
+#pragma unroll
+        for (int i = 0; i < S::kBlkW; ++i) {
+            const int r = 8 * (wave + S::kWaves * i) + lrow;
+            const int wrow = EPI == BEPI_SWIGLU && r >= 128 ? g.F + t.n0 + r - 128 : t.n0 + r;
+            voffW[i] = (uint32_t)wrow * (uint32_t)K + lchunk * 16;  // rows past Nw read 0
+        }
+        auto issue = [&](int kt) {
+            const uint32_t dst = lds0 + (kt % S::S) * S::kStage;
+            const uint32_t soff = (uint32_t)kt * S::RB;
+#pragma unroll
+            for (int i = 0; i < S::kBlkA; ++i)
+                dma16(rsA, dst + (wave + S::kWaves * i) * 1024, voffA[i], soff);
+#pragma unroll
+            for (int i = 0; i < S::kBlkW; ++i)
+                dma16(rsW, dst + S::kLdsA + (wave + S::kWaves * i) * 1024, voffW[i], soff);
+            dma_byte(rsS, dst + S::kLdsA + S::kLdsW + wave * 256, voffS, (uint32_t)kt);
+        };
+
+        f32x16 acc[S::kFM][S::kFN];
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    acc[i][j][v] = 0.0f;
+
+        __syncthreads();  // every wave is done with the previous tile's LDS
+        {
+            const size_t brow = (size_t)t.e * (g.Nw / kBlk);
+            const int c0 = t.n0 / kBlk;
+            const int c1 = EPI == BEPI_SWIGLU ? (g.F + t.n0) / kBlk : min(c0 + 1, g.Nw / kBlk - 1);
+            for (int q = tid; q < 2 * (k1 - k0); q += S::kThreads) {
+                const int h = q >= k1 - k0, kb = k0 + q - (h ? k1 - k0 : 0);
+                const size_t at = (brow + (h ? c1 : c0)) * nk + kb;
+                if constexpr (WF32)
+                    s_ws[h][kb] = __float_as_uint(static_cast<const float*>(g.Ws)[at]);
+                else
+                    s_ws[h][kb] = static_cast<const uint8_t*>(g.Ws)[at];
+            }
+        }
+        __syncthreads();
+        wait_vmcnt<0>();
+        for (int s = 0; s < S::S - 1; ++s)
+            if (k0 + s < k1)
+                issue(k0 + s);
+        for (int kt = k0; kt < k1; ++kt) {
+            if (kt + S::S - 1 < k1) {
+                issue(kt + S::S - 1);
+                wait_vmcnt<(S::S - 1) * S::kLoads>();
+            } else {
+                wait_vmcnt<0>();
+            }
+            lds_barrier();
+            const uint8_t* st = lds + (kt % S::S) * S::kStage;
+            int sa[S::kFM], sw[2];
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i)
+                sa[i] = *reinterpret_cast<const int*>(st + S::kLdsA + S::kLdsW +
+                                                      4 * (wm * S::kWaveM + i * 32 + (lane & 31)));
+            sw[0] = s_ws[0][kt];
+            sw[1] = s_ws[1][kt];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                i32x8 fa[S::kFM], fw[S::kFN];
+                const int c = 4 * kk + 2 * (lane >> 5);
+                auto rd = [&](int row, int ch, uint32_t at) {
+                    return *reinterpret_cast<const i32x4*>(st + at + bswz<S>(row, ch));
+                };
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) {
+                    const int row = (j / kHalfF) * 128 + wn * kHalfN + (j % kHalfF) * 32 + (lane & 31);
+                    fw[j].lo = rd(row, c, S::kLdsA);
+                    fw[j].hi = rd(row, c + 1, S::kLdsA);
+                }
+#pragma unroll
+                for (int i = 0; i < S::kFM; ++i) {
+                    const int row = wm * S::kWaveM + i * 32 + (lane & 31);
+                    fa[i].lo = rd(row, c, 0);
+                    fa[i].hi = rd(row, c + 1, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::kFN; ++j) {
+                        if constexpr (WF32) {
+                            f32x16 z = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                            z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[j], fa[i], z, 0, 0, 0, 127, 0,
+                                                                                sa[i]);
+                            const float s = __uint_as_float(sw[j / kHalfF]);
+#pragma unroll
+                            for (int v = 0; v < 16; ++v)
+                                acc[i][j][v] = fmaf(s, z[v], acc[i][j][v]);
+                        } else {
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                fw[j], fa[i], acc[i][j], 0, 0, 0, sw[j / kHalfF], 0, sa[i]);
+                        }
+                    }
+            }
+            lds_barrier();
+        }
+        if (slot < 0) {
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i)
+                block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * 1024), g);
+        } else {
+            float* dst = g.partial + (size_t)slot * S::kTileFloats;
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4*>(
+                            dst + ((((size_t)i * S::kWaves + wave) * S::kFN + j) * 4 + q) * 256 + lane * 4) =
+                            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                        acc[i][j][4 * q + 3]);
+        }
+    }
+#endif
+}
+
+// Second pass of the K split: block (split tile, row fragment) adds the parts
+// in part order and runs the epilogue.
+template <typename S, int EPI>
+__global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmArgs g, int G)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) uint8_t buf[S::WM * 32 * 1024];
+    __shared__ int32_t s_pref[kGemmMaxE + 1];
+    __shared__ int32_t s_wsum[S::kWaves];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
+    const int total = s_pref[g.E];
+    const int parts = block_parts(total, G, g.K / kBlk, true);
+    if (parts <= 1)
+        return;
+    const int tail = total % G, full = total - tail;
+    const int j = blockIdx.x / S::kFM, i = blockIdx.x % S::kFM;
+    if (j >= tail)
+        return;
+    const TileDec t = decode_tile<S>(full + j, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
+    f32x16 acc[S::kFN];
+#pragma unroll
+    for (int n = 0; n < S::kFN; ++n)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            acc[n][v] = 0.0f;
+    for (int part = 0; part < parts; ++part) {
+        const float* src = g.partial + (size_t)(j * parts + part) * S::kTileFloats +
+                           (size_t)(i * S::kWaves + wave) * S::kFN * 1024 + lane * 4;
+#pragma unroll
+        for (int n = 0; n < S::kFN; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 p = *reinterpret_cast<const float4*>(src + (n * 4 + q) * 256);
+                acc[n][4 * q] += p.x;
+                acc[n][4 * q + 1] += p.y;
+                acc[n][4 * q + 2] += p.z;
+                acc[n][4 * q + 3] += p.w;
+            }
+    }
+    block_store<S, EPI>(acc, i, t, buf, g);
+#endif
+}
+
+}  // namespace moe
+
+namespace {
+using namespace moe;
+
+typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
+typedef BlockShape<64, 1, 4, 2, 4> SmallShape;
+
+template <typename S, int EPI, bool WF32>
+hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
+{
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const long long ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    // upper bound on m-tiles: whole tiles plus one partial per expert
+    const long long mt = g.max_rows / S::BM + (long long)std::min(g.E, g.max_rows);
+    long long grid = ncu;
+    if (mt * ntn < grid && g.partial == nullptr)
+        grid = (mt * ntn + 7) / 8 * 8;
+    moe_block_gemm_kernel<S, EPI, WF32><<<dim3((unsigned)grid), dim3(S::kThreads), 0, stream>>>(g);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || g.partial == nullptr)
+        return err;
+    moe_block_tail_kernel<S, EPI>
+        <<<dim3(kBlkSplitSlots / 2 * S::kFM), dim3(S::kThreads), 0, stream>>>(g, (int)grid);
+    return hipGetLastError();
+}
+
+template <typename S>
+hipError_t launch_epi(int epi, bool wf32, const BlockGemmArgs& g, int ncu, hipStream_t s)
+{
+    if (epi == BEPI_RELU)
+        return wf32 ? launch_shape<S, BEPI_RELU, true>(g, ncu, s) : launch_shape<S, BEPI_RELU, false>(g, ncu, s);
+    if (epi == BEPI_SWIGLU)
+        return wf32 ? launch_shape<S, BEPI_SWIGLU, true>(g, ncu, s) : launch_shape<S, BEPI_SWIGLU, false>(g, ncu, s);
+    return wf32 ? launch_shape<S, BEPI_NONE, true>(g, ncu, s) : launch_shape<S, BEPI_NONE, false>(g, ncu, s);
+}
+
+template <typename ET, bool F32>
+void launch_quantize(const void* src, long long R, int K, int block_rows, uint8_t* codes, void* scales, hipStream_t s)
+{
+    typedef typename ET::storage T;
+    if (block_rows == 1) {
+        const long long blocks = R * (K / kBlk);
+        moe_quantize_rows_kernel<ET, F32>
+            <<<dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, s>>>((const T*)src, blocks, codes, scales);
+    } else {
+        const long long blocks = (R + kBlk - 1) / kBlk * (K / kBlk);
+        moe_quantize_tiles_kernel<ET, F32>
+            <<<dim3((unsigned)blocks), dim3(256), 0, s>>>((const T*)src, R, K, codes, scales);
+    }
+}
+}  // namespace
+
+// src: R rows of K values (dtype 0 fp32, 1 bf16), K a multiple of 128;
+// block_rows 1 or 128; scales fp32 numbers (f32) or E8M0 bytes.  R * K / 128
+// below 2^35.
+extern "C" hipError_t moe_launch_quantize_block(int dtype, const void* src, long long R, int K, int block_rows,
+                                                int f32, uint8_t* codes, void* scales, hipStream_t stream)
+{
+    if (R <= 0)
+        return hipSuccess;
+    if (dtype == 0)
+        f32 ? launch_quantize<f32_t, true>(src, R, K, block_rows, codes, scales, stream)
+            : launch_quantize<f32_t, false>(src, R, K, block_rows, codes, scales, stream);
+    else
+        f32 ? launch_quantize<bf16_t, true>(src, R, K, block_rows, codes, scales, stream)
+            : launch_quantize<bf16_t, false>(src, R, K, block_rows, codes, scales, stream);
+    return hipGetLastError();
+}
+
+// Bytes of the K split's partial tiles for this mean number of rows per expert.
+extern "C" size_t moe_block_gemm_partial_bytes(int mean_rows)
+{
+    return (size_t)kBlkSplitSlots * (mean_rows >= 128 ? LargeShape::kTileFloats : SmallShape::kTileFloats) * 4;
+}
+
+// epi 0: Y = bf16 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  wf32: fp32 weight scales.
+// mean_rows: expected rows per expert.  partial (nullable): the K split's
+// workspace, moe_block_gemm_partial_bytes bytes.
+extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint8_t* As,
+                                            const int32_t* gather, int gather_rows, const uint8_t* W, const void* Ws,
+                                            uint8_t* Hq, uint8_t* Hs, void* Y, const int32_t* offsets, int E, int K,
+                                            int Nw, int Nout, int F, int max_rows, int mean_rows, int ncu,
+                                            float* partial, hipStream_t stream)
+{
+    const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, (uint16_t*)Y, offsets, E, K, Nw, Nout, F,
+                             max_rows, K >= 2048 ? partial : nullptr};
+    if (mean_rows >= 128)
+        return launch_epi<LargeShape>(epi, wf32 != 0, g, ncu, stream);
+    return launch_epi<SmallShape>(epi, wf32 != 0, g, ncu, stream);
+}

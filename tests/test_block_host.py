@@ -1,0 +1,180 @@
+"""Host checks of the block-scaled FP8 experts and of the balance loss: sizes,
+refusals before anything is enqueued, and the 64-bit references themselves.
+No kernel is launched (these run without a GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import mixture_experts_layer_logit_amd as moe
+import _block_ref as ref
+
+FAKE = 1 << 20  # an aligned, never dereferenced address
+BIG = 1 << 40
+
+
+def status(fn, *args):
+    return getattr(moe.load(), fn)(*args)
+
+
+def prob(**kw):
+    a = dict(T=64, d=256, E=8, k=2, F=384, act="swiglu")
+    a.update(kw)
+    return moe.problem(a.pop("T"), a.pop("d"), a.pop("E"), a.pop("k"), a.pop("F"), **a)
+
+
+# ---------------------------------------------------------------- the references
+def test_reference_codes():
+    assert ref.POS[126] == 448 and ref.POS[1] == 2.0 ** -9 and len(ref.POS) == 127
+    assert list(ref.encode(np.array([1.0625, 1.1875, 448.0, -0.0, 2.0 ** -10, 3 * 2.0 ** -10]))) == [
+        0x38, 0x3A, 0x7E, 0x80, 0x00, 0x02]
+    try:
+        import torch
+    except ImportError:
+        return
+    v = np.random.default_rng(0).standard_normal(100000) * 20
+    t = torch.from_numpy(v).float()
+    assert np.array_equal(ref.encode(t.double().numpy()), t.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_reference_scales():
+    for a, e in ((0.0, 0), (448.0, 0), (448.0001, 1), (224.0, -1), (224.5, 0), (2.0 ** -200, -127), (1.0, -8)):
+        assert ref.exponent(a) == e
+    for a in np.exp(np.random.default_rng(1).uniform(-60, 60, 2000)):
+        e = int(ref.exponent(a))
+        assert a <= 448 * 2.0 ** e and a > 224 * 2.0 ** e
+
+
+def test_reference_gradient_by_differences():
+    g = np.random.default_rng(2)
+    z, idx = g.standard_normal((6, 4)), g.integers(0, 4, (6, 2))
+    off = np.array([0, 2, 2, 5])
+    for norm in (False, True):
+        _, _, dz, _ = ref.balance(z, idx, off, 0.6, 0.2, norm, 1.7)
+        assert np.all(np.isnan(dz[5]))
+        for t in range(5):
+            for e in range(4):
+                l = []
+                for s in (1e-5, -1e-5):
+                    zz = z.copy()
+                    zz[t, e] += s
+                    v = ref.balance(zz, idx, off, 0, 0, norm, 1.7)[1]
+                    l.append(0.6 * v[0] + 0.2 * v[1])
+                assert abs((l[0] - l[1]) / 2e-5 - dz[t, e]) < 1e-8
+
+
+# ---------------------------------------------------------------- refusals
+def quantise(src=FAKE, dt=moe.MOE_BF16, rows=8, K=256, br=1, codes=FAKE, scales=FAKE, kind=moe.MOE_SCALE_E8M0):
+    return status("moe_quantize_fp8_block", src, dt, rows, K, br, codes, scales, kind, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dt=2), moe.MOE_ERR_INVALID_ARG), (dict(kind=2), moe.MOE_ERR_INVALID_ARG), (dict(kind=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(br=0), moe.MOE_ERR_INVALID_ARG), (dict(br=64), moe.MOE_ERR_INVALID_ARG), (dict(rows=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(K=64), moe.MOE_ERR_UNSUPPORTED), (dict(K=192), moe.MOE_ERR_UNSUPPORTED), (dict(K=65536 + 128), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows=1 << 31), moe.MOE_ERR_UNSUPPORTED), (dict(rows=(1 << 31) - 1, K=65536), moe.MOE_ERR_UNSUPPORTED),
+    (dict(src=None), moe.MOE_ERR_INVALID_ARG), (dict(src=FAKE + 8), moe.MOE_ERR_INVALID_ARG),
+    (dict(codes=None), moe.MOE_ERR_INVALID_ARG), (dict(codes=FAKE + 8), moe.MOE_ERR_INVALID_ARG),
+    (dict(scales=None), moe.MOE_ERR_INVALID_ARG),
+    (dict(scales=FAKE + 2, kind=moe.MOE_SCALE_F32), moe.MOE_ERR_INVALID_ARG)])
+def test_quantise_refusals(kw, want):
+    assert quantise(**kw) == want
+    assert moe.load().moe_last_error()
+
+
+def test_quantise_of_no_rows():
+    assert quantise(rows=0, src=None, codes=None, scales=None) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("kw,want", [(dict(dtype="f32"), moe.MOE_ERR_UNSUPPORTED), (dict(d=320), moe.MOE_ERR_UNSUPPORTED),
+                                     (dict(F=448), moe.MOE_ERR_UNSUPPORTED), (dict(k=9, E=16), moe.MOE_ERR_UNSUPPORTED),
+                                     (dict(T=-1), moe.MOE_ERR_INVALID_ARG)])
+def test_layer_problem_refusals(kw, want):
+    p = prob(**kw)
+    n = ctypes.c_size_t()
+    assert status("moe_fp8_block_workspace_size", ctypes.byref(p), ctypes.byref(n)) == want
+    assert status("moe_expert_up_fp8_block", ctypes.byref(p), *[FAKE] * 6, 0, FAKE, FAKE, None, 0, None) == want
+    assert status("moe_expert_down_fp8_block", ctypes.byref(p), *[FAKE] * 5, 0, FAKE, None, 0, None) == want
+    assert status("moe_forward_fp8_block", ctypes.byref(p), *[FAKE] * 7, 0, FAKE, None, None, FAKE, BIG, None) == want
+
+
+def test_workspace_size_needs_its_result():
+    assert status("moe_fp8_block_workspace_size", ctypes.byref(prob()), None) == moe.MOE_ERR_INVALID_ARG
+    assert status("moe_balance_workspace_size", ctypes.byref(prob()), 1, None) == moe.MOE_ERR_INVALID_ARG
+
+
+UP = dict(aq=FAKE, as_=FAKE, src=FAKE, off=FAKE, w=FAKE, ws=FAKE, kind=0, hq=FAKE, hs=FAKE, work=None, n=0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(aq=None), 1), (dict(aq=FAKE + 4), 1), (dict(as_=None), 1), (dict(src=FAKE + 2), 1), (dict(off=None), 1),
+    (dict(off=FAKE + 1), 1), (dict(w=None), 1), (dict(w=FAKE + 8), 1), (dict(ws=None), 1),
+    (dict(ws=FAKE + 1, kind=1), 1), (dict(kind=7), 1), (dict(hq=None), 1), (dict(hq=FAKE + 8), 1), (dict(hs=None), 1),
+    (dict(work=FAKE, n=16), 3), (dict(work=FAKE + 8, n=BIG), 1)])
+def test_up_refusals(kw, want):
+    a = dict(UP, **kw)
+    assert status("moe_expert_up_fp8_block", ctypes.byref(prob()), a["aq"], a["as_"], a["src"], a["off"], a["w"], a["ws"],
+                  a["kind"], a["hq"], a["hs"], a["work"], a["n"], None) == want
+    assert moe.load().moe_last_error()
+
+
+def test_gather_beyond_32_bits_is_refused():
+    p = prob(T=1 << 24, d=256, E=8, k=1)
+    assert status("moe_expert_up_fp8_block", ctypes.byref(p), *[FAKE] * 6, 0, FAKE, FAKE, None, 0, None) == moe.MOE_ERR_UNSUPPORTED
+    assert status("moe_forward_fp8_block", ctypes.byref(p), *[FAKE] * 7, 0, FAKE, None, None, FAKE, BIG, None) == moe.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("at,bad,want", [(0, None, 1), (0, FAKE + 8, 1), (1, None, 1), (2, None, 1), (2, FAKE + 1, 1),
+                                         (3, FAKE + 8, 1), (4, None, 1), (5, 5, 1), (6, None, 1), (6, FAKE + 2, 1)])
+def test_down_refusals(at, bad, want):
+    a = [FAKE, FAKE, FAKE, FAKE, FAKE, 0, FAKE]
+    a[at] = bad
+    assert status("moe_expert_down_fp8_block", ctypes.byref(prob()), *a, None, 0, None) == want
+
+
+@pytest.mark.parametrize("at,bad,want", [(0, None, 1), (1, FAKE + 8, 1), (2, FAKE + 2, 1), (3, None, 1), (4, None, 1),
+                                         (5, None, 1), (6, None, 1), (7, 3, 1), (8, None, 1), (9, FAKE + 2, 1),
+                                         (11, None, 1), (12, 64, 3)])
+def test_layer_refusals(at, bad, want):
+    a = [FAKE] * 7 + [0, FAKE, None, None, FAKE, BIG]
+    a[at] = bad
+    assert status("moe_forward_fp8_block", ctypes.byref(prob()), *a, None) == want
+
+
+def test_layer_with_given_logits_needs_them():
+    a = [FAKE, None, None] + [FAKE] * 4 + [0, FAKE, None, None, FAKE, BIG]
+    assert status("moe_forward_fp8_block", ctypes.byref(prob()), *a, None) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_binding_checks_scale_types():
+    torch = pytest.importorskip("torch")
+    p = prob()
+    f, b, h = torch.zeros(4), torch.zeros(4, dtype=torch.uint8), torch.zeros(4, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        moe.moe_quantize_fp8_block(torch.zeros(2, 128), b, h, stream=0)
+    with pytest.raises(TypeError):
+        moe.moe_expert_up_fp8_block(p, b, f, None, b, b, b, b, b, stream=0)
+    with pytest.raises(TypeError):
+        moe.moe_expert_down_fp8_block(p, b, b, b, b, h, b, stream=0)
+    with pytest.raises(TypeError):
+        moe.moe_forward_fp8_block(p, b, None, None, b, b, b, f, b, stream=0)
+
+
+BAL = dict(logits=FAKE, idx=FAKE, off=FAKE, n=3, a=0.1, z=0.1, counts=FAKE, losses=FAKE, dz=FAKE, ws=FAKE, size=BIG)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(logits=None), 1), (dict(logits=FAKE + 2), 1), (dict(idx=None), 1), (dict(off=None), 1), (dict(off=FAKE + 1), 1),
+    (dict(n=0), 1), (dict(n=-4), 1), (dict(n=(1 << 20) + 1), 2), (dict(a=float("nan")), 1), (dict(z=float("inf")), 1),
+    (dict(counts=None), 1), (dict(losses=None), 1), (dict(dz=FAKE + 2), 1), (dict(ws=None), 1), (dict(size=8), 3)])
+def test_balance_refusals(kw, want):
+    b = dict(BAL, **kw)
+    assert status("moe_balance_loss", ctypes.byref(prob()), b["logits"], b["idx"], b["off"], b["n"], b["a"], b["z"],
+                  b["counts"], b["losses"], b["dz"], b["ws"], b["size"], None) == want
+    assert moe.load().moe_last_error()
+
+
+def test_balance_counts_beyond_32_bits_are_refused():
+    n = ctypes.c_size_t()
+    assert status("moe_balance_workspace_size", ctypes.byref(prob(E=1024, k=2)), 1 << 21, ctypes.byref(n)) == 2
+    assert status("moe_balance_workspace_size", ctypes.byref(prob(E=1024, k=2)), 1 << 20, ctypes.byref(n)) == 0

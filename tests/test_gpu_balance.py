@@ -1,0 +1,209 @@
+"""moe_balance_loss through the C ABI against the 64-bit definition
+(tests/_block_ref.py) and against differences of the loss."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_logit_amd as moe
+import _block_ref as ref
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def make(T, E, k, seed=0, scale=1.5):
+    g = np.random.Generator(np.random.PCG64(seed + 31 * T + E))
+    z = (g.standard_normal((T, E)) * scale).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    return g, z, idx
+
+
+def call(p, z, idx, off, a, c, grad=True, fill=0xFF, stream=None):
+    S = 1 if off is None else len(off) - 1
+    T, E = z.shape
+    counts = torch.full((S, E), -1, dtype=torch.int32, device="cuda")
+    losses = torch.full((2,), float("nan"), device="cuda")
+    dz = torch.full((T, E), 9.0, device="cuda") if grad else None
+    ws = torch.empty(moe.moe_balance_workspace_size(p, S), dtype=torch.uint8, device="cuda").fill_(fill)
+    moe.moe_balance_loss(p, dev(z), dev(idx), None if off is None else dev(off), counts, losses, dz, a, c, ws, stream)
+    torch.cuda.synchronize()
+    return counts.cpu().numpy(), losses.cpu().numpy(), dz.cpu().numpy() if grad else None
+
+
+def cuts(T, S, kind, g):
+    if kind == "none":
+        return None
+    end = T if kind == "full" else T - T // 4
+    start = 0 if kind != "late" else T // 5
+    inner = np.sort(g.integers(start, end + 1, S - 1)) if S > 1 else np.zeros(0, int)
+    return np.concatenate([[start], inner, [end]]).astype(np.int32)
+
+
+@pytest.mark.parametrize("normalize,lam", [(False, 1.0), (True, 1.0), (True, 2.5)])
+@pytest.mark.parametrize("T,E,k,S,kind", [
+    (1, 1, 1, 1, "none"), (1, 8, 2, 1, "none"), (5, 2, 1, 5, "full"), (64, 8, 2, 1, "none"), (100, 7, 3, 4, "padded"),
+    (257, 33, 2, 6, "late"), (300, 64, 8, 3, "full"), (1031, 65, 4, 9, "padded"), (500, 128, 1, 40, "padded"),
+    (77, 160, 8, 2, "full"), (129, 256, 8, 3, "late"), (64, 500, 6, 2, "padded"), (65, 1024, 8, 3, "full"),
+    (9000, 16, 2, 3, "padded"), (40000, 8, 2, 5, "padded"), (700, 4, 1, 600, "full")])
+def test_against_the_definition(T, E, k, S, kind, normalize, lam):
+    print(f"[balance] T={T} E={E} k={k} S={S} {kind} normalize={normalize} lam={lam}", flush=True)
+    g, z, idx = make(T, E, k)
+    off = cuts(T, S, kind, g)
+    p = moe.problem(T, 64, E, k, 64, normalize=normalize, lam=lam)
+    counts, losses, dz = call(p, z, idx, off, 0.7, 0.3)
+    o = np.array([0, T]) if off is None else off
+    c, l, want, bound = ref.balance(z, idx, o, 0.7, 0.3, normalize, lam)
+    assert np.array_equal(counts, c)
+    held = ~np.isnan(want[:, 0])
+    assert np.all(dz[~held] == 9.0)
+    over = np.abs(dz[held] - want[held]) - bound[held]
+    assert np.all(over <= 0), f"{over.max():.3e} beyond the bound"
+    # each token's term within 4 (spread + 64) U24 of its own, all of one sign
+    eps = 4 * ((z.max(axis=1) - z.min(axis=1)).max() * max(1.0, lam) * (4 if normalize else 1) + 64) * ref.U24
+    assert np.all(np.abs(losses - l) <= eps * (l + 1e-3))
+    again = call(p, z, idx, off, 0.7, 0.3, fill=0)
+    assert np.array_equal(again[1], losses) and np.array_equal(again[2], dz)
+    only = call(p, z, idx, off, 0.7, 0.3, grad=False)
+    assert np.array_equal(only[0], c) and np.array_equal(only[1], losses)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_gradient_against_differences(normalize):
+    T, E, k = 7, 5, 2
+    g, z, idx = make(T, E, k, seed=3)
+    off = np.array([0, 3, 6], np.int32)
+    p = moe.problem(T, 64, E, k, 64, normalize=normalize, lam=1.3)
+    dz = call(p, z, idx, off, 0.9, 0.4)[2]
+    h = 1e-5
+    for t in range(6):
+        for e in range(E):
+            v = []
+            for sign in (1, -1):
+                zz = z.astype(np.float64)
+                zz[t, e] += sign * h
+                l = ref.balance(zz, idx, off, 0, 0, normalize, 1.3)[1]
+                v.append(0.9 * l[0] + 0.4 * l[1])
+            # central differences: error h^2 times third derivatives of order 1,
+            # and 2^-52 / h of rounding; the fp32 gradient 1e-6 of its largest
+            assert abs((v[0] - v[1]) / (2 * h) - dz[t, e]) <= 1e-8 + 4e-6 * np.abs(dz[:6]).max()
+
+
+def test_equal_to_the_router_statistics():
+    """One sequence of every token: the values of moe_router_stats."""
+    T, E, k = 333, 12, 2
+    g, z, idx = make(T, E, k)
+    p = moe.problem(T, 64, E, k, 64, normalize=True)
+    ws = torch.empty(moe.moe_workspace_size(p), dtype=torch.uint8, device="cuda")
+    counts, offsets = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    slot, src = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T * k, dtype=torch.int32, device="cuda")
+    moe.moe_permute(p, dev(idx), None, counts, offsets, slot, src, None, ws)
+    frac, mean = torch.empty(E, device="cuda"), torch.empty(E, device="cuda")
+    sc = torch.empty(3, device="cuda")
+    moe.moe_router_stats(p, dev(z), counts, offsets, frac, mean, sc, ws)
+    c, l, _ = call(p, z, idx, None, 0.0, 0.0)
+    assert np.array_equal(c[0], counts.cpu().numpy())
+    assert np.all(np.abs(l - sc.cpu().numpy()[:2]) <= 1e-5 * l)
+
+
+def test_masked_logits():
+    """-inf logits (experts closed to a token), a token with none open, and the
+    largest and lowest finite numbers beside ordinary ones."""
+    T, E, k = 40, 9, 2
+    g, z, idx = make(T, E, k)
+    z[g.random((T, E)) < 0.3] = -np.inf
+    z[5] = -np.inf
+    z[6] = -np.inf
+    z[6, 3] = 0.25
+    z[7, 2] = np.finfo(np.float32).min
+    z[8] = np.finfo(np.float32).min / 4
+    off = np.array([0, 10, 40], np.int32)
+    z_coef = 0.0  # lse of the lowest numbers squared is beyond fp32: only the balance term here
+    p = moe.problem(T, 64, E, k, 64)
+    counts, losses, dz = call(p, z, idx, off, 0.5, z_coef)
+    c, l, want, bound = ref.balance(z, idx, off, 0.5, z_coef)
+    assert np.array_equal(counts, c)
+    assert np.all(np.isfinite(dz)) and np.all(dz[~np.isfinite(z)] == 0) and np.all(dz[5] == 0)
+    assert np.all(np.abs(dz - want) <= bound + 1e-9)
+    z[8], z[7, 2] = 0.5, -30.0
+    counts, losses, dz = call(p, z, idx, off, 0.5, 0.2)
+    c, l, want, bound = ref.balance(z, idx, off, 0.5, 0.2)
+    assert np.all(np.abs(dz - want) <= bound)
+    assert np.all(np.abs(losses - l) <= 1e-4 * np.abs(l))
+
+
+def test_equal_logits_under_the_normalisation():
+    T, E, k = 12, 6, 2
+    z = np.full((T, E), 3.25, np.float32)
+    idx = np.tile(np.array([[0, 1]], np.int32), (T, 1))
+    p = moe.problem(T, 64, E, k, 64, normalize=True)
+    counts, losses, dz = call(p, z, idx, None, 1.0, 0.0)
+    assert np.all(dz == 0) and abs(losses[0] - 1.0) <= 1e-6
+
+
+def test_indices_out_of_range_are_skipped():
+    T, E, k = 20, 5, 2
+    g, z, idx = make(T, E, k)
+    idx[3] = [-1, E]
+    idx[4, 1] = 1 << 30
+    p = moe.problem(T, 64, E, k, 64)
+    counts, losses, dz = call(p, z, idx, None, 0.5, 0.1)
+    c, l, want, bound = ref.balance(z, idx, np.array([0, T]), 0.5, 0.1)
+    assert np.array_equal(counts, c) and np.all(np.abs(dz - want) <= bound)
+
+
+def test_no_tokens():
+    p = moe.problem(0, 64, 5, 2, 64)
+    counts = torch.full((3, 5), 4, dtype=torch.int32, device="cuda")
+    losses = torch.full((2,), 4.0, device="cuda")
+    ws = torch.empty(moe.moe_balance_workspace_size(p, 3), dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(p, None, None, torch.zeros(4, dtype=torch.int32, device="cuda"), counts, losses, None, 1.0, 1.0, ws)
+    torch.cuda.synchronize()
+    assert not counts.any() and not losses.any()
+    # tokens, but every sequence empty
+    p = moe.problem(6, 64, 5, 2, 64)
+    g, z, idx = make(6, 5, 2)
+    c, l, dz = call(p, z, idx, np.array([2, 2, 2], np.int32), 1.0, 1.0)
+    assert not c.any() and not l.any() and np.all(dz == 9.0)
+
+
+def test_graph_replay_and_streams():
+    T, E, k, S = 900, 24, 3, 4
+    g, z, idx = make(T, E, k)
+    p = moe.problem(T, 64, E, k, 64, normalize=True)
+    off = dev(cuts(T, S, "padded", g))
+    zt, it = dev(z), dev(idx)
+    counts = torch.empty(S, E, dtype=torch.int32, device="cuda")
+    losses, dz = torch.empty(2, device="cuda"), torch.zeros(T, E, device="cuda")
+    ws = torch.empty(moe.moe_balance_workspace_size(p, S), dtype=torch.uint8, device="cuda")
+
+    def run(s):
+        moe.moe_balance_loss(p, zt, it, off, counts, losses, dz, 0.3, 0.2, ws, s)
+
+    def take():
+        torch.cuda.synchronize()
+        return [t.cpu().numpy().copy() for t in (counts, losses, dz)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    run(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run(s)
+    for rep in range(4):
+        zt.mul_(0.9)
+        it.copy_(torch.roll(it, 1, 0))
+        ws.fill_(0xFF if rep % 2 else 0)
+        run(None)
+        want = take()
+        for t in (counts, losses, dz):
+            t.fill_(5)
+        dz.copy_(dev(want[2]))
+        ws.fill_(0x7F)
+        graph.replay()
+        for a, b in zip(take(), want):
+            assert np.array_equal(a, b), f"replay {rep}"
