@@ -66,7 +66,7 @@ hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint
                                  int gather_rows, const uint8_t* W, const void* Ws, uint8_t* Hq, uint8_t* Hs, void* Y,
                                  const int32_t* offsets, int E, int K, int Nw, int Nout, int F, int max_rows,
                                  int mean_rows, int ncu, float* partial, hipStream_t stream);
-size_t moe_balance_scratch_bytes(int T, int S);
+size_t moe_balance_scratch_bytes(void);
 hipError_t moe_launch_balance(const float* logits, const int32_t* topk_idx, const int32_t* offsets, int S, int T,
                               int E, int k, int normalize, float lambda, float aux_coef, float z_coef,
                               int32_t* counts, float* losses, float* dlogits, void* scratch, hipStream_t stream);
@@ -1197,7 +1197,7 @@ moe_status moe_balance_workspace_size(const moe_problem* p, int32_t n_seq, size_
     CHECK(check_balance(p, n_seq));
     if (!bytes)
         return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = round_up(moe_balance_scratch_bytes(p->T, n_seq));
+    *bytes = round_up(moe_balance_scratch_bytes());
     return ok();
 }
 
@@ -1220,7 +1220,7 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
         if (dlogits)
             CHECK(check_ptr(dlogits, "dlogits", 4));
     }
-    const size_t need = round_up(moe_balance_scratch_bytes(p->T, n_seq));
+    const size_t need = round_up(moe_balance_scratch_bytes());
     if (ws_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
     CHECK(check_ptr(ws, "ws", 16));
