@@ -10,6 +10,7 @@
 // Activation scales are E8M0 bytes (b stands for 2^(b - 127)); weight scales
 // are E8M0 bytes or fp32 numbers.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "fp8.h"
@@ -130,15 +131,17 @@ struct BlockShape {
     static constexpr int kWavesPerSimd = kWaves / 4;
     static constexpr int kWaveM = BM / WM, kWaveN = BN / WN;
     static constexpr int kFM = kWaveM / 32, kFN = kWaveN / 32;
+    static constexpr int kRows = 1024 / RB;  // tile rows of a 1 KB load
     static constexpr int kLdsA = BM * RB, kLdsW = BN * RB;
-    static constexpr int kScl = kThreads * 4;  // scales of the slice's activation rows, a dword each
+    static constexpr int kScl = kThreads * 4;  // scales of the stage's activation rows, a dword each
     static constexpr int kStage = kLdsA + kLdsW + kScl;
-    static constexpr int kBlkA = BM / 8 / kWaves, kBlkW = BN / 8 / kWaves;  // 1 KB loads per wavefront and slice
+    static constexpr int kBlkA = BM / kRows / kWaves, kBlkW = BN / kRows / kWaves;  // loads per wavefront and stage
     static constexpr int kLoads = kBlkA + kBlkW + 1;
     static constexpr int kTileFloats = BM * BN;
     static_assert(kFN % 2 == 0, "a wavefront takes rows of both weight halves");
-    static_assert(kWaves % 4 == 0 && BM % (8 * kWaves) == 0 && kThreads >= BM, "loads split evenly");
-    static_assert((S - 1) * kLoads <= 63, "vmcnt range");
+    static_assert(kWaves % 4 == 0 && BM % (kRows * kWaves) == 0 && kThreads >= BM, "loads split evenly");
+    static_assert(kBlkW % 2 == 0, "a load lies in one weight half");
+    static_assert(S >= 2 && (S - 1) * kLoads <= 63, "vmcnt range");
     static_assert(2 * (WM * 32) * BN * 4 <= S * kStage, "two staged row fragments fit the stages");
 };
 
@@ -157,10 +160,18 @@ struct BlockGemmArgs {
     float* partial;  // nullable: no K split
 };
 
+// LDS offset of 16-byte chunk c of tile row `row`: the chunk index XOR-ed with
+// the row pair's number (two rows fill the 64 banks once), so that one chunk of
+// 16 consecutive rows touches every bank once.
+template <typename S>
+__device__ __forceinline__ int bswz_term(int row)
+{
+    return (row >> 1) & 7;
+}
 template <typename S>
 __device__ __forceinline__ uint32_t bswz(int row, int c)
 {
-    return row * S::RB + ((c ^ ((row >> 1) & 7)) << 4);
+    return row * S::RB + ((c ^ bswz_term<S>(row)) << 4);
 }
 
 // One dword per lane from a byte of buffer `rsrc` at voff + soff, zero
@@ -215,8 +226,9 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float u = acc[j][4 * g4 + q];
-                if constexpr (kGlu)
-                    v[q] = u / (1.0f + __expf(-u)) * acc[j + kHalfF][4 * g4 + q];
+                if constexpr (kGlu)  // u / (1 + e^-u) times the up value
+                    v[q] = u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) *
+                           acc[j + kHalfF][4 * g4 + q];
                 else if constexpr (EPI == BEPI_RELU)
                     v[q] = fmaxf(u, 0.0f);
                 else
@@ -225,10 +237,9 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
             const int byte = col * kEl;
             uint8_t* dst = buf + r * kRowBytes + (((byte >> 4) ^ (r & kSwz)) << 4) + (byte & 15);
             if constexpr (kEl == 2) {
-                uint2 o;
-                o.x = f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16);
-                o.y = f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16);
-                *reinterpret_cast<uint2*>(dst) = o;
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                typedef float f32x4v __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<bf16x4*>(dst) = __builtin_convertvector(f32x4v{v[0], v[1], v[2], v[3]}, bf16x4);
             } else {
                 *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
             }
@@ -296,6 +307,12 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
     const int K = g.K, nk = K / kBlk;
     const uint32_t lds0 = lds_addr(lds);
     constexpr int kHalfN = S::kWaveN / 2, kHalfF = S::kFN / 2;
+    // LDS offsets of this lane's first fragments in a stage; the k-step and the
+    // 16-byte half flip single bits of them, fragments 32 rows apart keep their
+    // swizzle
+    const uint32_t rdA = bswz<S>(wm * S::kWaveM + (lane & 31), 2 * (lane >> 5));
+    const uint32_t rdW = S::kLdsA + bswz<S>(wn * kHalfN + (lane & 31), 2 * (lane >> 5));
+    const uint32_t rdS = S::kLdsA + S::kLdsW + 4 * (wm * S::kWaveM + (lane & 31));
 
     const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
     const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
@@ -322,63 +339,77 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         }
         const TileDec t = decode_tile<S>(tile, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
 
-        // lane's place in a 1 KB load of 8 rows: row lane / 8, physical chunk
-        // lane % 8; a wavefront's loads all have the parity of its number
-        const int lrow = lane / 8;
-        const int lchunk = (lane % 8) ^ ((((wave & 1) << 2) + (lrow >> 1)) & 7);
+        // lane's place in a 1 KB load of kRows rows: row lane / kCh, physical
+        // chunk lane % kCh; the swizzle term is the same in all of a
+        // wavefront's loads (their row blocks all have the parity of its number)
+        constexpr int kCh = S::RB / 16;
+        const int lrow = S::kRows * wave + lane / kCh;
+        const uint32_t lchunk = (uint32_t)((lane % kCh) ^ bswz_term<S>(lrow)) * 16;
         i32x4 rsA, rsS;
         uint32_t voffA[S::kBlkA], voffS;
         const int srow = wave * kWave + lane;  // the tile row whose scale this lane loads
         if (g.gather) {
             rsA = make_rsrc(g.A, (uint32_t)g.gather_rows * (uint32_t)K);
             rsS = make_rsrc(g.As, (uint32_t)g.gather_rows * (uint32_t)nk);
+            auto source = [&](int r) {
+                const int src = r < t.rows ? g.gather[t.row0 + r] : -1;
+                return src < g.gather_rows ? src : -1;
+            };
 #pragma unroll
             for (int i = 0; i < S::kBlkA; ++i) {
-                const int r = 8 * (wave + S::kWaves * i) + lrow;
-                const int src = r < t.rows ? g.gather[t.row0 + r] : -1;
-                voffA[i] = src >= 0 && src < g.gather_rows ? (uint32_t)src * (uint32_t)K + lchunk * 16 : 0xf0000000u;
+                const int src = source(lrow + S::kRows * S::kWaves * i);
+                voffA[i] = src >= 0 ? (uint32_t)src * (uint32_t)K + lchunk : 0xf0000000u;
             }
-            const int src = srow < t.rows ? g.gather[t.row0 + srow] : -1;
-            voffS = src >= 0 && src < g.gather_rows ? (uint32_t)src * (uint32_t)nk : 0xf0000000u;
+            const int src = source(srow);
+            voffS = src >= 0 ? (uint32_t)src * (uint32_t)nk : 0xf0000000u;
         } else {
             rsA = make_rsrc(g.A + (size_t)t.row0 * K, (uint32_t)t.rows * (uint32_t)K);
             rsS = make_rsrc(g.As + (size_t)t.row0 * nk, (uint32_t)t.rows * (uint32_t)nk);
 #pragma unroll
             for (int i = 0; i < S::kBlkA; ++i)
-                voffA[i] = (uint32_t)(8 * (wave + S::kWaves * i) + lrow) * (uint32_t)K + lchunk * 16;
+                voffA[i] = (uint32_t)(lrow + S::kRows * S::kWaves * i) * (uint32_t)K + lchunk;
             voffS = srow < t.rows ? (uint32_t)srow * (uint32_t)nk : 0xf0000000u;
         }
+        // the weight rows' offsets: one lane part, and a scalar part per load;
+        // the second half of the last tile may lie behind the matrix
         const i32x4 rsW = make_rsrc(g.W + (size_t)t.e * g.Nw * K, (uint32_t)g.Nw * (uint32_t)K);
-        uint32_t voffW[S::kBlkW];
+        const uint32_t voffW = (uint32_t)lrow * (uint32_t)K + lchunk;
+        const uint32_t half1 = EPI == BEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + 128);
+        const bool second = (int)half1 < g.Nw;
+
+        // Loads [n0, n1) of slice q's kLoads into LDS stage st.  Past the last
+        // slice (and behind the matrix's last row) they read offset 0 of empty
+        // buffers: no memory traffic, the same count.
+        auto issue = [&](int q, int st, int n0, int n1) {
+            const uint32_t at = lds0 + st * S::kStage, dst = at + wave * 1024;
+            const bool in = q < k1;
+            i32x4 ra = rsA, rw0 = rsW, rw1 = rsW, rs = rsS;
+            ra[2] = in ? ra[2] : 0;
+            rw0[2] = in ? rw0[2] : 0;
+            rw1[2] = in && second ? rw1[2] : 0;
+            rs[2] = in ? rs[2] : 0;
+            const uint32_t soff = in ? (uint32_t)q * S::RB : 0, kb = in ? (uint32_t)q : 0;
+            const uint32_t row0 = in ? (uint32_t)t.n0 * (uint32_t)K : 0;
+            const uint32_t row1 = in && second ? half1 * (uint32_t)K : 0, step = in ? S::kRows * S::kWaves * (uint32_t)K : 0;
 #pragma unroll
-        for (int i = 0; i < S::kBlkW; ++i) {
-            const int r = 8 * (wave + S::kWaves * i) + lrow;
-            const int wrow = EPI == BEPI_SWIGLU && r >= 128 ? g.F + t.n0 + r - 128 : t.n0 + r;
-            voffW[i] = (uint32_t)wrow * (uint32_t)K + lchunk * 16;  // rows past Nw read 0
-        }
-        auto issue = [&](int kt) {
-            const uint32_t dst = lds0 + (kt % S::S) * S::kStage;
-            const uint32_t soff = (uint32_t)kt * S::RB;
-#pragma unroll
-            for (int i = 0; i < S::kBlkA; ++i)
-                dma16(rsA, dst + (wave + S::kWaves * i) * 1024, voffA[i], soff);
-#pragma unroll
-            for (int i = 0; i < S::kBlkW; ++i)
-                dma16(rsW, dst + S::kLdsA + (wave + S::kWaves * i) * 1024, voffW[i], soff);
-            dma_byte(rsS, dst + S::kLdsA + S::kLdsW + wave * 256, voffS, (uint32_t)kt);
+            for (int p = 0; p < S::kLoads; ++p) {
+                if (p < n0 || p >= n1)
+                    continue;
+                // weights, which come from farthest away, then scales, then activations
+                const int n = (p + S::kBlkA) % S::kLoads;
+                const int w = n - S::kBlkA;
+                if (w < 0)
+                    dma16(ra, dst + S::kWaves * n * 1024, voffA[w < 0 ? n : 0], soff);
+                else if (w < S::kBlkW / 2)
+                    dma16(rw0, dst + S::kLdsA + S::kWaves * w * 1024, voffW, soff + row0 + w * step);
+                else if (w < S::kBlkW)
+                    dma16(rw1, dst + S::kLdsA + S::kWaves * w * 1024, voffW,
+                          second ? soff + row1 + (w - S::kBlkW / 2) * step : 0);
+                else
+                    dma_byte(rs, at + S::kLdsA + S::kLdsW + wave * 256, voffS, kb);
+            }
         };
-
-        f32x16 acc[S::kFM][S::kFN];
-#pragma unroll
-        for (int i = 0; i < S::kFM; ++i)
-#pragma unroll
-            for (int j = 0; j < S::kFN; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    acc[i][j][v] = 0.0f;
-
-        __syncthreads();  // every wave is done with the previous tile's LDS
-        {
+        auto load_weight_scales = [&]() {
             const size_t brow = (size_t)t.e * (g.Nw / kBlk);
             const int c0 = t.n0 / kBlk;
             const int c1 = EPI == BEPI_SWIGLU ? (g.F + t.n0) / kBlk : min(c0 + 1, g.Nw / kBlk - 1);
@@ -390,71 +421,171 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                 else
                     s_ws[h][kb] = static_cast<const uint8_t*>(g.Ws)[at];
             }
-        }
-        __syncthreads();
-        wait_vmcnt<0>();
-        for (int s = 0; s < S::S - 1; ++s)
-            if (k0 + s < k1)
-                issue(k0 + s);
-        for (int kt = k0; kt < k1; ++kt) {
-            if (kt + S::S - 1 < k1) {
-                issue(kt + S::S - 1);
-                wait_vmcnt<(S::S - 1) * S::kLoads>();
-            } else {
-                wait_vmcnt<0>();
-            }
-            lds_barrier();
-            const uint8_t* st = lds + (kt % S::S) * S::kStage;
-            int sa[S::kFM], sw[2];
+        };
+
+        f32x16 acc[S::kFM][S::kFN];
 #pragma unroll
-            for (int i = 0; i < S::kFM; ++i)
-                sa[i] = *reinterpret_cast<const int*>(st + S::kLdsA + S::kLdsW +
-                                                      4 * (wm * S::kWaveM + i * 32 + (lane & 31)));
-            sw[0] = s_ws[0][kt];
-            sw[1] = s_ws[1][kt];
+        for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                i32x8 fa[S::kFM], fw[S::kFN];
-                const int c = 4 * kk + 2 * (lane >> 5);
-                auto rd = [&](int row, int ch, uint32_t at) {
-                    return *reinterpret_cast<const i32x4*>(st + at + bswz<S>(row, ch));
-                };
+            for (int j = 0; j < S::kFN; ++j)
 #pragma unroll
-                for (int j = 0; j < S::kFN; ++j) {
-                    const int row = (j / kHalfF) * 128 + wn * kHalfN + (j % kHalfF) * 32 + (lane & 31);
-                    fw[j].lo = rd(row, c, S::kLdsA);
-                    fw[j].hi = rd(row, c + 1, S::kLdsA);
+                for (int v = 0; v < 16; ++v)
+                    acc[i][j][v] = 0.0f;
+
+        wait_vmcnt<0>();  // the previous tile's stores are out of the count
+        __syncthreads();  // and every wave is done with its LDS
+        load_weight_scales();
+#pragma unroll
+        for (int q = 0; q < S::S; ++q)
+            issue(k0 + q, q, 0, S::kLoads);
+        wait_vmcnt<(S::S - 1) * S::kLoads>();
+        lds_barrier();
+
+        struct Frags {
+            i32x8 w[S::kFN], a[S::kFM];
+        };
+        // The K loop for a wavefront whose first L row fragments hold rows of the
+        // segment (the others are neither read nor multiplied).  A slice takes two
+        // k-steps of 64 values.  In the first, the second's fragments are read as
+        // fast as the LDS gives them; behind a barrier the stage is free then and
+        // takes the loads of slice kt + S, weights first.  Between the two k-steps
+        // slice kt + 1 has to be there (a second barrier).  So a load has 1 1/4
+        // slices (S = 2) to arrive.  Against one barrier between the k-steps and a
+        // load time of one slice, 8 wavefronts of 128 x 64 each, same card: 16
+        // experts of 512 rows 915 -> 845 us, one of 8192 rows 790 -> 793 us (4096 x
+        // 28672 weights; the weights of one expert stay in the caches).  Loads
+        // spread over fewer MFMAs, all behind the second barrier or half of them in
+        // the next slice, 64-byte slices in four stages, and touching the weight
+        // lines two slices ahead were slower by 2 to 15 %; so were flags in LDS in
+        // place of the barriers, and 4 wavefronts of 128 x 128 each.
+        auto kloop = [&](auto lc) {
+            constexpr int L = decltype(lc)::value;
+            constexpr int NM = L * S::kFN, NR = L > 0 ? 2 * (L + S::kFN) : 0;
+            Frags f0, f1;
+            int sa[S::kFM], sw[2], swn[2];
+            auto read = [&](int r, Frags& nx, uint32_t st, int kk) {
+                const int n = r / 2, h = r % 2;  // fragment, 16-byte half
+                const uint32_t x = (uint32_t)(kk * 64) ^ (uint32_t)(h * 16);
+                const i32x4 v = *reinterpret_cast<const i32x4*>(
+                    lds + st + (n < S::kFN ? (rdW ^ x) + ((n / kHalfF) * 128 + (n % kHalfF) * 32) * S::RB
+                                           : (rdA ^ x) + (n - S::kFN) * 32 * S::RB));
+                i32x8& dst = n < S::kFN ? nx.w[n] : nx.a[n - S::kFN];
+                if (h)
+                    dst.hi = v;
+                else
+                    dst.lo = v;
+            };
+            auto read_scale = [&](int i, uint32_t st) {
+                sa[i] = *reinterpret_cast<const int*>(lds + st + rdS + i * 128);
+            };
+            // One k-step (64 values of K): the MFMAs on the fragments in f, and
+            // between them the LDS reads of the next k-step's fragments into nx
+            // (k-step kk of stage st) and, where LAST, the row scales of the next
+            // slice and the loads of slice q into stage lst.  An MFMA runs for 64
+            // cycles, in which its wavefront can issue the few instructions that
+            // follow it.
+            constexpr int kEarly = S::kBlkW;                       // loads issued in a slice's first k-step: the weights'
+            constexpr int kFree = NM >= 8 ? 3 : NM > 2 ? NM / 2 : NM;  // MFMAs behind which its reads are spread
+            constexpr int kBar = NM >= 8 ? 3 : NM > 0 ? kFree - 1 : 0;  // the one behind which the stage is free
+            auto kstep = [&](const Frags& f, Frags& nx, uint32_t st, int kk, auto last, int q, int lst) {
+                constexpr bool LAST = decltype(last)::value;
+                // reads behind an MFMA
+                constexpr int kOver = LAST ? NM : kFree;
+                constexpr int kPer = kOver > 0 && (NR + kOver - 1) / kOver > 2 ? (NR + kOver - 1) / kOver : 2;
+                if constexpr (NM == 0) {
+                    if (!LAST)
+                        lds_barrier();
+                    issue(q, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
                 }
 #pragma unroll
-                for (int i = 0; i < S::kFM; ++i) {
-                    const int row = wm * S::kWaveM + i * 32 + (lane & 31);
-                    fa[i].lo = rd(row, c, 0);
-                    fa[i].hi = rd(row, c + 1, 0);
-                }
+                for (int m = 0; m < NM; ++m) {
+                    const int i = m / S::kFN, j = m % S::kFN;
+                    if constexpr (WF32) {
+                        f32x16 z = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                        z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[j], f.a[i], z, 0, 0, 0, 127, 0, sa[i]);
+                        const float s = __int_as_float(sw[j / kHalfF]);
 #pragma unroll
-                for (int i = 0; i < S::kFM; ++i)
+                        for (int v = 0; v < 16; ++v)
+                            acc[i][j][v] = fmaf(s, z[v], acc[i][j][v]);
+                    } else {
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[j], f.a[i], acc[i][j], 0, 0,
+                                                                                    0, sw[j / kHalfF], 0, sa[i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int j = 0; j < S::kFN; ++j) {
-                        if constexpr (WF32) {
-                            f32x16 z = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                            z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[j], fa[i], z, 0, 0, 0, 127, 0,
-                                                                                sa[i]);
-                            const float s = __uint_as_float(sw[j / kHalfF]);
-#pragma unroll
-                            for (int v = 0; v < 16; ++v)
-                                acc[i][j][v] = fmaf(s, z[v], acc[i][j][v]);
-                        } else {
-                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                fw[j], fa[i], acc[i][j], 0, 0, 0, sw[j / kHalfF], 0, sa[i]);
+                    for (int r = 0; r < NR; ++r)
+                        if (r / kPer == m)
+                            read(r, nx, st, kk);
+                    if constexpr (LAST) {
+                        if (j == S::kFN - 1)
+                            read_scale(i, st);
+                        constexpr int kLate = S::kLoads - kEarly;
+                        issue(q, lst, kEarly + m * kLate / NM, kEarly + (m + 1) * kLate / NM);
+                    } else {
+                        // every wavefront's reads of the stage are done: it is free
+                        if (m == kBar)
+                            lds_barrier();
+                        if (m >= kBar) {
+                            constexpr int kLeft = NM - kBar > 0 ? NM - kBar : 1;
+                            issue(q, lst, (m - kBar) * kEarly / kLeft, (m - kBar + 1) * kEarly / kLeft);
                         }
                     }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            constexpr std::integral_constant<bool, false> first{};
+            constexpr std::integral_constant<bool, true> last{};
+            // in the order of the loop's own reads: the waits at its head are the
+            // stricter of the two
+            sw[0] = s_ws[0][k0];
+            sw[1] = s_ws[1][k0];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                constexpr int kPer = (NR + NM - 1) / (NM > 0 ? NM : 1) > 2 ? (NR + NM - 1) / (NM > 0 ? NM : 1) : 2;
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (r / kPer == m)
+                        read(r, f0, 0, 0);
+                if (m % S::kFN == S::kFN - 1)
+                    read_scale(m / S::kFN, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            lds_barrier();
-        }
+            int cur = 0;  // stage of slice kt
+            for (int kt = k0; kt < k1; ++kt) {
+                const int nxt = cur + 1 == S::S ? 0 : cur + 1;
+                kstep(f0, f1, cur * S::kStage, 1, first, kt + S::S, cur);
+                // slice kt + 1 has to be there
+                wait_vmcnt<(S::S - 2) * S::kLoads + kEarly>();
+                lds_barrier();
+                swn[0] = s_ws[0][min(kt + 1, k1 - 1)];
+                swn[1] = s_ws[1][min(kt + 1, k1 - 1)];
+                kstep(f1, f0, nxt * S::kStage, 0, last, kt + S::S, cur);
+                sw[0] = swn[0];
+                sw[1] = swn[1];
+                cur = nxt;
+            }
+        };
+        // rows past the segment's end are not stored: a wavefront leaves out the
+        // fragments that hold none (a copy of the loop for each count)
+        const int live = min(max((t.rows - wm * S::kWaveM + 31) / 32, 0), S::kFM);
+        if (S::kFM == 1 || live == S::kFM)
+            kloop(std::integral_constant<int, S::kFM>{});
+        else if (S::kFM > 3 && live == 3)
+            kloop(std::integral_constant<int, (S::kFM > 3 ? 3 : 1)>{});
+        else if (S::kFM > 2 && live == 2)
+            kloop(std::integral_constant<int, (S::kFM > 2 ? 2 : 1)>{});
+        else if (live == 1)
+            kloop(std::integral_constant<int, 1>{});
+        else
+            kloop(std::integral_constant<int, 0>{});
+        wait_vmcnt<0>();  // the loads behind the last slice fetch nothing, but write zeros to the stages
+        lds_barrier();
         if (slot < 0) {
 #pragma unroll
             for (int i = 0; i < S::kFM; ++i)
-                block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * 1024), g);
+                if (i * 32 < t.rows)
+                    block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * 1024), g);
         } else {
             float* dst = g.partial + (size_t)slot * S::kTileFloats;
 #pragma unroll
@@ -523,8 +654,18 @@ __global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmAr
 namespace {
 using namespace moe;
 
-typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
-typedef BlockShape<64, 1, 4, 2, 4> SmallShape;
+#ifndef BLK_LARGE
+#define BLK_LARGE 256, 2, 4, 2, 8
+#endif
+#ifndef BLK_SMALL
+#define BLK_SMALL 64, 1, 4, 3, 4
+#endif
+#ifndef BLK_F32
+#define BLK_F32 128, 2, 4, 3, 8
+#endif
+typedef BlockShape<BLK_LARGE> LargeShape;
+typedef BlockShape<BLK_SMALL> SmallShape;
+typedef BlockShape<BLK_F32> F32Shape;
 
 template <typename S, int EPI, bool WF32>
 hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
@@ -545,14 +686,14 @@ hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename S>
-hipError_t launch_epi(int epi, bool wf32, const BlockGemmArgs& g, int ncu, hipStream_t s)
+template <typename S, bool WF32>
+hipError_t launch_epi(int epi, const BlockGemmArgs& g, int ncu, hipStream_t s)
 {
     if (epi == BEPI_RELU)
-        return wf32 ? launch_shape<S, BEPI_RELU, true>(g, ncu, s) : launch_shape<S, BEPI_RELU, false>(g, ncu, s);
+        return launch_shape<S, BEPI_RELU, WF32>(g, ncu, s);
     if (epi == BEPI_SWIGLU)
-        return wf32 ? launch_shape<S, BEPI_SWIGLU, true>(g, ncu, s) : launch_shape<S, BEPI_SWIGLU, false>(g, ncu, s);
-    return wf32 ? launch_shape<S, BEPI_NONE, true>(g, ncu, s) : launch_shape<S, BEPI_NONE, false>(g, ncu, s);
+        return launch_shape<S, BEPI_SWIGLU, WF32>(g, ncu, s);
+    return launch_shape<S, BEPI_NONE, WF32>(g, ncu, s);
 }
 
 template <typename ET, bool F32>
@@ -605,7 +746,9 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
 {
     const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, (uint16_t*)Y, offsets, E, K, Nw, Nout, F,
                              max_rows, K >= 2048 ? partial : nullptr};
-    if (mean_rows >= 128)
-        return launch_epi<LargeShape>(epi, wf32 != 0, g, ncu, stream);
-    return launch_epi<SmallShape>(epi, wf32 != 0, g, ncu, stream);
+    if (wf32)
+        return mean_rows >= 128 ? launch_epi<F32Shape, true>(epi, g, ncu, stream)
+                                : launch_epi<SmallShape, true>(epi, g, ncu, stream);
+    return mean_rows >= 128 ? launch_epi<LargeShape, false>(epi, g, ncu, stream)
+                            : launch_epi<SmallShape, false>(epi, g, ncu, stream);
 }
