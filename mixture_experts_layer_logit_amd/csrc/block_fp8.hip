@@ -195,6 +195,13 @@ __device__ __forceinline__ int block_parts(int total, int G, int nk, bool enable
     return max(1, min(min(kBlkMaxParts, min(G, kBlkSplitSlots) / tail), nk / kBlkMinPart));
 }
 
+// silu(u) v, silu(u) = u / (1 + e^-u); the exponential and the reciprocal to
+// within a step or two of fp32, which the E4M3 code behind them does not see.
+__device__ __forceinline__ float glu(float u, float v)
+{
+    return u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) * v;
+}
+
 // Epilogue of row fragment i of every wavefront (WM bands of 32 rows), whose
 // accumulators are acc[0 .. kFN): staged in LDS as [band row][column] (16-byte
 // chunks XOR-swizzled by the row), then taken row by row.  Activation
@@ -226,9 +233,8 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float u = acc[j][4 * g4 + q];
-                if constexpr (kGlu)  // u / (1 + e^-u) times the up value
-                    v[q] = u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) *
-                           acc[j + kHalfF][4 * g4 + q];
+                if constexpr (kGlu)
+                    v[q] = glu(u, acc[j + kHalfF][4 * g4 + q]);
                 else if constexpr (EPI == BEPI_RELU)
                     v[q] = fmaxf(u, 0.0f);
                 else
@@ -238,8 +244,7 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
             uint8_t* dst = buf + r * kRowBytes + (((byte >> 4) ^ (r & kSwz)) << 4) + (byte & 15);
             if constexpr (kEl == 2) {
                 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                typedef float f32x4v __attribute__((ext_vector_type(4)));
-                *reinterpret_cast<bf16x4*>(dst) = __builtin_convertvector(f32x4v{v[0], v[1], v[2], v[3]}, bf16x4);
+                *reinterpret_cast<bf16x4*>(dst) = __builtin_convertvector(f32x4{v[0], v[1], v[2], v[3]}, bf16x4);
             } else {
                 *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
             }
@@ -375,38 +380,47 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         const i32x4 rsW = make_rsrc(g.W + (size_t)t.e * g.Nw * K, (uint32_t)g.Nw * (uint32_t)K);
         const uint32_t voffW = (uint32_t)lrow * (uint32_t)K + lchunk;
         const uint32_t half1 = EPI == BEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + 128);
-        const bool second = (int)half1 < g.Nw;
+        const bool second = EPI == BEPI_SWIGLU || (int)half1 < g.Nw;
+        const uint32_t voffW1 = second ? voffW : 0xf0000000u, row0 = (uint32_t)t.n0 * (uint32_t)K;
+        const uint32_t row1 = second ? half1 * (uint32_t)K : 0, step = S::kRows * S::kWaves * (uint32_t)K;
+        // Small tiles, which stream weights: every tile of columns starts at
+        // another slice.  Where rows lie a multiple of 2048 bytes apart, blocks
+        // that all read the same slice at a time meet in few of the memory's
+        // channels (weights 4096 wide, 8 experts, 16 rows: 202 -> 166 us, 4.65 ->
+        // 5.67 TB/s; 6144, 8192 and 12288 wide 13 to 30 % faster; 14336 wide no
+        // difference; 2048, 2560 and 3584 wide 3 to 6 % slower, left alone).  The
+        // tile decides, so the sums keep their order from run to run.
+        constexpr bool kRotate = S::kWaves == 4;
+        int rot = 0;
+        if (kRotate && K >= 4096 && K % 2048 == 0)
+            rot = (t.n0 / tile_cols * 5) % (k1 - k0);
+        auto slice_of = [&](int q) {
+            if constexpr (kRotate)
+                return q + rot >= k1 ? q + rot - (k1 - k0) : q + rot;
+            else
+                return q;
+        };
 
-        // Loads [n0, n1) of slice q's kLoads into LDS stage st.  Past the last
-        // slice (and behind the matrix's last row) they read offset 0 of empty
-        // buffers: no memory traffic, the same count.
+        // Loads [n0, n1) of the kLoads of slice number q into LDS stage st.
+        // Weights, which come from farthest away, then scales, then activations;
+        // the half behind the matrix's last row reads behind the buffer: zeros.
         auto issue = [&](int q, int st, int n0, int n1) {
             const uint32_t at = lds0 + st * S::kStage, dst = at + wave * 1024;
-            const bool in = q < k1;
-            i32x4 ra = rsA, rw0 = rsW, rw1 = rsW, rs = rsS;
-            ra[2] = in ? ra[2] : 0;
-            rw0[2] = in ? rw0[2] : 0;
-            rw1[2] = in && second ? rw1[2] : 0;
-            rs[2] = in ? rs[2] : 0;
-            const uint32_t soff = in ? (uint32_t)q * S::RB : 0, kb = in ? (uint32_t)q : 0;
-            const uint32_t row0 = in ? (uint32_t)t.n0 * (uint32_t)K : 0;
-            const uint32_t row1 = in && second ? half1 * (uint32_t)K : 0, step = in ? S::kRows * S::kWaves * (uint32_t)K : 0;
+            const uint32_t kb = (uint32_t)slice_of(q), soff = kb * S::RB;
 #pragma unroll
             for (int p = 0; p < S::kLoads; ++p) {
                 if (p < n0 || p >= n1)
                     continue;
-                // weights, which come from farthest away, then scales, then activations
-                const int n = (p + S::kBlkA) % S::kLoads;
-                const int w = n - S::kBlkA;
-                if (w < 0)
-                    dma16(ra, dst + S::kWaves * n * 1024, voffA[w < 0 ? n : 0], soff);
-                else if (w < S::kBlkW / 2)
-                    dma16(rw0, dst + S::kLdsA + S::kWaves * w * 1024, voffW, soff + row0 + w * step);
-                else if (w < S::kBlkW)
-                    dma16(rw1, dst + S::kLdsA + S::kWaves * w * 1024, voffW,
-                          second ? soff + row1 + (w - S::kBlkW / 2) * step : 0);
+                if (p < S::kBlkW / 2)
+                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW, soff + row0 + p * step);
+                else if (p < S::kBlkW)
+                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == BEPI_SWIGLU ? voffW : voffW1,
+                          soff + row1 + (p - S::kBlkW / 2) * step);
+                else if (p == S::kBlkW)
+                    dma_byte(rsS, at + S::kLdsA + S::kLdsW + wave * 256, voffS, kb);
                 else
-                    dma_byte(rs, at + S::kLdsA + S::kLdsW + wave * 256, voffS, kb);
+                    dma16(rsA, dst + S::kWaves * (p - S::kBlkW - 1) * 1024, voffA[p > S::kBlkW ? p - S::kBlkW - 1 : 0],
+                          soff);
             }
         };
         auto load_weight_scales = [&]() {
@@ -437,8 +451,12 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         load_weight_scales();
 #pragma unroll
         for (int q = 0; q < S::S; ++q)
-            issue(k0 + q, q, 0, S::kLoads);
-        wait_vmcnt<(S::S - 1) * S::kLoads>();
+            if (k0 + q < k1)
+                issue(k0 + q, q, 0, S::kLoads);
+        if (k1 - k0 >= S::S)
+            wait_vmcnt<(S::S - 1) * S::kLoads>();
+        else
+            wait_vmcnt<0>();
         lds_barrier();
 
         struct Frags {
@@ -481,21 +499,22 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
             // One k-step (64 values of K): the MFMAs on the fragments in f, and
             // between them the LDS reads of the next k-step's fragments into nx
             // (k-step kk of stage st) and, where LAST, the row scales of the next
-            // slice and the loads of slice q into stage lst.  An MFMA runs for 64
-            // cycles, in which its wavefront can issue the few instructions that
-            // follow it.
+            // slice; where LOADS, the loads of slice q into stage lst.  An MFMA runs
+            // for 64 cycles, in which its wavefront can issue the few instructions
+            // that follow it.
             constexpr int kEarly = S::kBlkW;                       // loads issued in a slice's first k-step: the weights'
             constexpr int kFree = NM >= 8 ? 3 : NM > 2 ? NM / 2 : NM;  // MFMAs behind which its reads are spread
             constexpr int kBar = NM >= 8 ? 3 : NM > 0 ? kFree - 1 : 0;  // the one behind which the stage is free
-            auto kstep = [&](const Frags& f, Frags& nx, uint32_t st, int kk, auto last, int q, int lst) {
-                constexpr bool LAST = decltype(last)::value;
+            auto kstep = [&](const Frags& f, Frags& nx, uint32_t st, int kk, auto last, auto loads, int q, int lst) {
+                constexpr bool LAST = decltype(last)::value, LOADS = decltype(loads)::value;
                 // reads behind an MFMA
                 constexpr int kOver = LAST ? NM : kFree;
                 constexpr int kPer = kOver > 0 && (NR + kOver - 1) / kOver > 2 ? (NR + kOver - 1) / kOver : 2;
                 if constexpr (NM == 0) {
-                    if (!LAST)
+                    if (!LAST && LOADS)
                         lds_barrier();
-                    issue(q, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
+                    if (LOADS)
+                        issue(q, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
                 }
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
@@ -519,9 +538,10 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                     if constexpr (LAST) {
                         if (j == S::kFN - 1)
                             read_scale(i, st);
-                        constexpr int kLate = S::kLoads - kEarly;
-                        issue(q, lst, kEarly + m * kLate / NM, kEarly + (m + 1) * kLate / NM);
-                    } else {
+                        constexpr int kLate = S::kLoads - kEarly, kSafe = NM > 0 ? NM : 1;
+                        if constexpr (LOADS)
+                            issue(q, lst, kEarly + m * kLate / kSafe, kEarly + (m + 1) * kLate / kSafe);
+                    } else if constexpr (LOADS) {
                         // every wavefront's reads of the stage are done: it is free
                         if (m == kBar)
                             lds_barrier();
@@ -533,12 +553,12 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
-            constexpr std::integral_constant<bool, false> first{};
-            constexpr std::integral_constant<bool, true> last{};
+            constexpr std::integral_constant<bool, false> no{};
+            constexpr std::integral_constant<bool, true> yes{};
             // in the order of the loop's own reads: the waits at its head are the
             // stricter of the two
-            sw[0] = s_ws[0][k0];
-            sw[1] = s_ws[1][k0];
+            sw[0] = s_ws[0][slice_of(k0)];
+            sw[1] = s_ws[1][slice_of(k0)];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -552,19 +572,26 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                 __builtin_amdgcn_sched_barrier(0);
             }
             int cur = 0;  // stage of slice kt
-            for (int kt = k0; kt < k1; ++kt) {
+            auto slice = [&](int kt, auto loads) {
+                constexpr bool LOADS = decltype(loads)::value;
                 const int nxt = cur + 1 == S::S ? 0 : cur + 1;
-                kstep(f0, f1, cur * S::kStage, 1, first, kt + S::S, cur);
+                kstep(f0, f1, cur * S::kStage, 1, no, loads, kt + S::S, cur);
                 // slice kt + 1 has to be there
-                wait_vmcnt<(S::S - 2) * S::kLoads + kEarly>();
+                wait_vmcnt<LOADS ? (S::S - 2) * S::kLoads + kEarly : 0>();
                 lds_barrier();
-                swn[0] = s_ws[0][min(kt + 1, k1 - 1)];
-                swn[1] = s_ws[1][min(kt + 1, k1 - 1)];
-                kstep(f1, f0, nxt * S::kStage, 0, last, kt + S::S, cur);
+                const int sn = slice_of(min(kt + 1, k1 - 1));
+                swn[0] = s_ws[0][sn];
+                swn[1] = s_ws[1][sn];
+                kstep(f1, f0, nxt * S::kStage, 0, yes, loads, kt + S::S, cur);
                 sw[0] = swn[0];
                 sw[1] = swn[1];
                 cur = nxt;
-            }
+            };
+            int kt = k0;
+            for (; kt + S::S < k1; ++kt)
+                slice(kt, yes);
+            for (; kt < k1; ++kt)  // nothing is left to load
+                slice(kt, no);
         };
         // rows past the segment's end are not stored: a wavefront leaves out the
         // fragments that hold none (a copy of the loop for each count)
@@ -579,7 +606,6 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
             kloop(std::integral_constant<int, 1>{});
         else
             kloop(std::integral_constant<int, 0>{});
-        wait_vmcnt<0>();  // the loads behind the last slice fetch nothing, but write zeros to the stages
         lds_barrier();
         if (slot < 0) {
 #pragma unroll
@@ -587,11 +613,13 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                 if (i * 32 < t.rows)
                     block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * 1024), g);
         } else {
+            // rows past the segment's end stay unwritten
             float* dst = g.partial + (size_t)slot * S::kTileFloats;
 #pragma unroll
             for (int i = 0; i < S::kFM; ++i)
+                if (wm * S::kWaveM + i * 32 + (lane & 31) < t.rows)
 #pragma unroll
-                for (int j = 0; j < S::kFN; ++j)
+                    for (int j = 0; j < S::kFN; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         *reinterpret_cast<float4*>(
@@ -625,13 +653,16 @@ __global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmAr
     if (j >= tail)
         return;
     const TileDec t = decode_tile<S>(full + j, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
+    if (i * 32 >= t.rows)
+        return;
+    const bool live = (wave / S::WN) * S::kWaveM + i * 32 + (lane & 31) < t.rows;
     f32x16 acc[S::kFN];
 #pragma unroll
     for (int n = 0; n < S::kFN; ++n)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
             acc[n][v] = 0.0f;
-    for (int part = 0; part < parts; ++part) {
+    for (int part = 0; live && part < parts; ++part) {
         const float* src = g.partial + (size_t)(j * parts + part) * S::kTileFloats +
                            (size_t)(i * S::kWaves + wave) * S::kFN * 1024 + lane * 4;
 #pragma unroll
@@ -654,18 +685,39 @@ __global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmAr
 namespace {
 using namespace moe;
 
-#ifndef BLK_LARGE
-#define BLK_LARGE 256, 2, 4, 2, 8
-#endif
-#ifndef BLK_SMALL
-#define BLK_SMALL 64, 1, 4, 3, 4
-#endif
-#ifndef BLK_F32
-#define BLK_F32 128, 2, 4, 3, 8
-#endif
-typedef BlockShape<BLK_LARGE> LargeShape;
-typedef BlockShape<BLK_SMALL> SmallShape;
-typedef BlockShape<BLK_F32> F32Shape;
+// Tiles, picked by the mean rows per expert, which the host knows without
+// reading the offsets (16 experts, SwiGLU 4096 x 4096, up / down in us):
+//   rows     64-row tile   96-row      128-row     256-row
+//     40       104 / 56   105 / 57    134 / 69    137 / 71
+//     72       124 / 68   109 / 60    133 / 71    139 / 73
+//    160       173 / 89   144 / 76    152 / 80    148 / 79
+//    256       255 / 131  199 / 101   187 / 106   179 / 112
+//    512       456 / 221  355 / 177   323 / 165   270 / 148
+// The 96-row tile below 192 rows, the 256-row one from there on; where 96-row
+// tiles leave CUs without one, the 64-row tile (16 experts, ReLU 1024 x 2048, 88
+// rows each: 13 / 14 us against 16 / 16).  fp32 weight scales need a product of
+// their own for each block before it is added, registers that the 256-row tile
+// does not have: 128 rows there.  32-row tiles and weights loaded straight into
+// the operands' registers, without LDS, were slower or equal at every size.
+typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
+typedef BlockShape<128, 2, 4, 3, 8> LargeF32Shape;
+typedef BlockShape<96, 1, 4, 3, 4> MediumShape;
+typedef BlockShape<64, 1, 4, 3, 4> SmallShape;
+constexpr int kLargeRows = 192;
+
+// Whether the last round is split along K.  The split costs a second launch
+// (about 4 us), so it is left out where K is short, and where the tiles expected
+// (rows spread evenly over min(rows, E) experts) fill more than half of the only
+// round: one token of two experts, 224 tiles of 256 CUs, 54.9 -> 51.8 us without.
+template <typename S>
+bool split_pays(const BlockGemmArgs& g, long long ntn, int ncu)
+{
+    if (g.K < 2048)
+        return false;
+    const long long busy = std::min(g.E, g.max_rows);
+    const long long tiles = busy * std::max(1ll, (g.max_rows / busy + S::BM - 1) / S::BM) * ntn;
+    return tiles <= ncu / 2 || tiles > ncu;
+}
 
 template <typename S, int EPI, bool WF32>
 hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
@@ -674,6 +726,8 @@ hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
     const long long ntn = (g.Nout + tile_cols - 1) / tile_cols;
     // upper bound on m-tiles: whole tiles plus one partial per expert
     const long long mt = g.max_rows / S::BM + (long long)std::min(g.E, g.max_rows);
+    if (!split_pays<S>(g, ntn, ncu))
+        g.partial = nullptr;
     long long grid = ncu;
     if (mt * ntn < grid && g.partial == nullptr)
         grid = (mt * ntn + 7) / 8 * 8;
@@ -732,7 +786,7 @@ extern "C" hipError_t moe_launch_quantize_block(int dtype, const void* src, long
 // Bytes of the K split's partial tiles for this mean number of rows per expert.
 extern "C" size_t moe_block_gemm_partial_bytes(int mean_rows)
 {
-    return (size_t)kBlkSplitSlots * (mean_rows >= 128 ? LargeShape::kTileFloats : SmallShape::kTileFloats) * 4;
+    return (size_t)kBlkSplitSlots * 4 * (mean_rows >= kLargeRows ? LargeShape::kTileFloats : MediumShape::kTileFloats);
 }
 
 // epi 0: Y = bf16 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  wf32: fp32 weight scales.
@@ -745,10 +799,16 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
                                             float* partial, hipStream_t stream)
 {
     const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, (uint16_t*)Y, offsets, E, K, Nw, Nout, F,
-                             max_rows, K >= 2048 ? partial : nullptr};
-    if (wf32)
-        return mean_rows >= 128 ? launch_epi<F32Shape, true>(epi, g, ncu, stream)
-                                : launch_epi<SmallShape, true>(epi, g, ncu, stream);
-    return mean_rows >= 128 ? launch_epi<LargeShape, false>(epi, g, ncu, stream)
-                            : launch_epi<SmallShape, false>(epi, g, ncu, stream);
+                             max_rows, partial};
+    if (mean_rows >= kLargeRows)
+        return wf32 ? launch_epi<LargeF32Shape, true>(epi, g, ncu, stream)
+                    : launch_epi<LargeShape, false>(epi, g, ncu, stream);
+    const int tile_cols = epi == BEPI_SWIGLU ? 128 : 256;
+    const long long tiles = (long long)std::min(E, max_rows) * ((mean_rows + 95) / 96 + (mean_rows == 0)) *
+                            ((Nout + tile_cols - 1) / tile_cols);
+    if (tiles < ncu)
+        return wf32 ? launch_epi<SmallShape, true>(epi, g, ncu, stream)
+                    : launch_epi<SmallShape, false>(epi, g, ncu, stream);
+    return wf32 ? launch_epi<MediumShape, true>(epi, g, ncu, stream)
+                : launch_epi<MediumShape, false>(epi, g, ncu, stream);
 }
