@@ -442,7 +442,8 @@ moe_status moe_expert_down_fp8_block(const moe_problem* p, const uint8_t* hq, co
                                      void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
 /* The whole layer: route and permute as moe_forward, quantise x per 1 x 128
- * block, both expert layers on codes, combine.  Other arguments as
+ * block, both expert layers on codes, combine.  The expert outputs stay in fp32
+ * up to the combine: y is rounded to bf16 once.  Other arguments as
  * moe_forward.  Needs ws_bytes >= moe_fp8_block_workspace_size; T*d >=
  * 0xF0000000 returns MOE_ERR_UNSUPPORTED. */
 moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void* Wg, const float* bg,

@@ -66,6 +66,8 @@ hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint
                                  int gather_rows, const uint8_t* W, const void* Ws, uint8_t* Hq, uint8_t* Hs, void* Y,
                                  const int32_t* offsets, int E, int K, int Nw, int Nout, int F, int max_rows,
                                  int mean_rows, int ncu, float* partial, hipStream_t stream);
+hipError_t moe_launch_combine_rows(const float* rows, const int32_t* slot, const float* topk_w, int T, int d, int k,
+                                   int max_rows, void* y, hipStream_t stream);
 size_t moe_balance_scratch_bytes(void);
 hipError_t moe_launch_balance(const float* logits, const int32_t* topk_idx, const int32_t* offsets, int S, int T,
                               int E, int k, int normalize, float lambda, float aux_coef, float z_coef,
@@ -490,7 +492,7 @@ LayoutFp8Block layout_fp8_block_of(const moe_problem* p)
     L.xs = take(T * (d / 128));
     L.hq = take(T * k * F);
     L.hs = take(T * k * (F / 128));
-    L.y_perm = take(T * k * d * 2);
+    L.y_perm = take(T * k * d * 4);  // fp32 in the layer
     L.total = off;
     return L;
 }
@@ -527,10 +529,10 @@ moe_status do_up_fp8_block(const moe_problem* p, const uint8_t* aq, const uint8_
 }
 
 moe_status do_down_fp8_block(const moe_problem* p, const uint8_t* hq, const uint8_t* hs, const int32_t* offsets,
-                             const uint8_t* W2q, const void* w2s, int32_t w_scale, void* y_perm, float* partial,
-                             hipStream_t s)
+                             const uint8_t* W2q, const void* w2s, int32_t w_scale, void* y_perm, bool f32,
+                             float* partial, hipStream_t s)
 {
-    return hip_status(moe_launch_block_gemm(0, w_scale == MOE_SCALE_F32, hq, hs, nullptr, 0, W2q, w2s, nullptr,
+    return hip_status(moe_launch_block_gemm(f32 ? 3 : 0, w_scale == MOE_SCALE_F32, hq, hs, nullptr, 0, W2q, w2s, nullptr,
                                             nullptr, y_perm, offsets, p->E, p->F, p->d, p->d, p->F, p->T * p->k,
                                             mean_rows_of(p), cu_count(), partial, s),
                       "block FP8 expert down launch");
@@ -1138,7 +1140,7 @@ moe_status moe_expert_down_fp8_block(const moe_problem* p, const uint8_t* hq, co
     if (ws)
         CHECK(check_ws_fp8_block(p, ws, ws_bytes));
     float* partial = ws ? at<float>(ws, layout_fp8_block_of(p).partial) : nullptr;
-    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, partial, (hipStream_t)stream));
+    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, false, partial, (hipStream_t)stream));
     return ok();
 }
 
@@ -1187,8 +1189,9 @@ moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void
                      "permute launch"));
     CHECK(hip_status(moe_launch_quantize_block(1, x, p->T, p->d, 1, 0, xq, xs, s), "block FP8 quantisation launch"));
     CHECK(do_up_fp8_block(p, xq, xs, src_token, offsets, W1q, w1s, w_scale, hq, hs, partial, s));
-    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, partial, s));
-    CHECK(do_combine(p, y_perm, slot, topk_w, nullptr, y, s));
+    CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, true, partial, s));
+    CHECK(hip_status(moe_launch_combine_rows(at<float>(ws, L.y_perm), slot, topk_w, p->T, p->d, p->k, p->T * p->k, y,
+                                             s), "combine launch"));
     return ok();
 }
 

@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256) void moe_quantize_tiles_kernel(const typename 
 // that scales them, so the matrix core applies both scales of a block to the
 // products itself.  The weight tile is its first operand, the activation tile
 // its second: a lane's accumulators are 4 consecutive columns of one row.
-enum { BEPI_NONE = 0, BEPI_RELU = 1, BEPI_SWIGLU = 2 };
+enum { BEPI_NONE = 0, BEPI_RELU = 1, BEPI_SWIGLU = 2, BEPI_F32 = 3 };  // bf16 rows, hidden codes (2), fp32 rows
 
 constexpr int kBlkMaxParts = 16;     // K parts of a tail tile
 constexpr int kBlkSplitSlots = 256;  // partial tiles the workspace holds
@@ -154,7 +154,7 @@ struct BlockGemmArgs {
     const void* Ws;    // [E][Nw / 128][K / 128]
     uint8_t* Hq;       // codes of the hidden rows [.][Nout] (activation epilogues)
     uint8_t* Hs;       // their scales [.][Nout / 128]
-    uint16_t* Y;       // bf16 rows [.][Nout] (plain epilogue)
+    void* Y;           // bf16 or fp32 rows [.][Nout] (plain epilogues)
     const int32_t* offsets;
     int E, K, Nw, Nout, F, max_rows;
     float* partial;  // nullable: no K split
@@ -213,6 +213,7 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
                                             const BlockGemmArgs& g)
 {
     constexpr bool kGlu = EPI == BEPI_SWIGLU;
+    constexpr bool kRows32 = EPI == BEPI_F32, kPlain = EPI == BEPI_NONE || kRows32;
     constexpr int HC = kGlu ? 128 : 256;  // output columns of the tile
     constexpr int kRows = S::WM * 32;
     constexpr int kEl = EPI == BEPI_NONE ? 2 : 4;
@@ -250,15 +251,16 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
             }
         }
     lds_barrier();
-    if constexpr (EPI == BEPI_NONE) {
-        constexpr int kChunks = kRowBytes / 16;
+    if constexpr (kPlain) {
+        constexpr int kChunks = kRowBytes / 16, kPer = 16 / kEl;
 #pragma unroll
         for (int it = 0; it < kRows * kChunks / S::kThreads; ++it) {
             const int c = tid + it * S::kThreads;
             const int rr = c / kChunks, q = c % kChunks;
             const int m = (rr / 32) * S::kWaveM + i * 32 + (rr % 32);
-            if (m < t.rows && t.n0 + q * 8 < g.Nout)
-                *reinterpret_cast<uint4*>(g.Y + (size_t)(t.row0 + m) * g.Nout + t.n0 + q * 8) =
+            if (m < t.rows && t.n0 + q * kPer < g.Nout)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.Y) +
+                                          ((size_t)(t.row0 + m) * g.Nout + t.n0 + q * kPer) * kEl) =
                     *reinterpret_cast<const uint4*>(buf + rr * kRowBytes + ((q ^ (rr & kSwz)) << 4));
         }
     } else {
@@ -680,6 +682,49 @@ __global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmAr
 #endif
 }
 
+// ---------------------------------------------------------------- combine
+// y[t] = sum over the kept choices j, in order, of topk_w[t,j] * rows[slot[t,j]]
+// in fp32, rounded to bf16 once: the layer keeps the expert outputs in fp32, so
+// that y has one rounding (rounded to bf16 on the way they put its error at 1.55
+// times that; the rows' traffic is 2 % of a prompt layer's time).  A thread takes
+// 8 columns of a token; the loads of all its choices leave together.  Slots
+// outside [0, max_rows) are dropped choices.
+template <int KMAX>
+__global__ __launch_bounds__(256) void moe_combine_rows_kernel(const float* __restrict__ rows,
+                                                               const int32_t* __restrict__ slot,
+                                                               const float* __restrict__ topk_w, int T, int d, int k,
+                                                               int max_rows, uint16_t* __restrict__ y)
+{
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int per = d / 8;
+    const int t = (int)(at / per), c = (int)(at % per) * 8;
+    if (t >= T)
+        return;
+    float f[KMAX][8], w[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+        const int s = j < k ? slot[(size_t)t * k + j] : -1;
+        const bool kept = s >= 0 && s < max_rows;
+        w[j] = kept ? topk_w[(size_t)t * k + j] : 0.0f;
+        if (kept) {
+            load8(rows + (size_t)s * d + c, f[j]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                f[j][q] = 0.0f;
+        }
+    }
+    float acc[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        acc[q] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KMAX; ++j)
+            acc[q] = fmaf(w[j], f[j][q], acc[q]);
+    }
+    store8(y + (size_t)t * d + c, acc);
+}
+
 }  // namespace moe
 
 namespace {
@@ -747,6 +792,8 @@ hipError_t launch_epi(int epi, const BlockGemmArgs& g, int ncu, hipStream_t s)
         return launch_shape<S, BEPI_RELU, WF32>(g, ncu, s);
     if (epi == BEPI_SWIGLU)
         return launch_shape<S, BEPI_SWIGLU, WF32>(g, ncu, s);
+    if (epi == BEPI_F32)
+        return launch_shape<S, BEPI_F32, WF32>(g, ncu, s);
     return launch_shape<S, BEPI_NONE, WF32>(g, ncu, s);
 }
 
@@ -789,7 +836,7 @@ extern "C" size_t moe_block_gemm_partial_bytes(int mean_rows)
     return (size_t)kBlkSplitSlots * 4 * (mean_rows >= kLargeRows ? LargeShape::kTileFloats : MediumShape::kTileFloats);
 }
 
-// epi 0: Y = bf16 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  wf32: fp32 weight scales.
+// epi 0: Y = bf16 rows, 3: Y = fp32 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  wf32: fp32 weight scales.
 // mean_rows: expected rows per expert.  partial (nullable): the K split's
 // workspace, moe_block_gemm_partial_bytes bytes.
 extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint8_t* As,
@@ -798,7 +845,7 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
                                             int Nw, int Nout, int F, int max_rows, int mean_rows, int ncu,
                                             float* partial, hipStream_t stream)
 {
-    const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, (uint16_t*)Y, offsets, E, K, Nw, Nout, F,
+    const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F,
                              max_rows, partial};
     if (mean_rows >= kLargeRows)
         return wf32 ? launch_epi<LargeF32Shape, true>(epi, g, ncu, stream)
@@ -811,4 +858,23 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
                     : launch_epi<SmallShape, false>(epi, g, ncu, stream);
     return wf32 ? launch_epi<MediumShape, true>(epi, g, ncu, stream)
                 : launch_epi<MediumShape, false>(epi, g, ncu, stream);
+}
+
+// rows: fp32 [max_rows][d]; d a multiple of 8, k <= 8.
+extern "C" hipError_t moe_launch_combine_rows(const float* rows, const int32_t* slot, const float* topk_w, int T,
+                                              int d, int k, int max_rows, void* y, hipStream_t stream)
+{
+    using namespace moe;
+    const long long threads = (long long)T * (d / 8);
+    const dim3 grid((unsigned)((threads + 255) / 256)), block(256);
+    uint16_t* out = (uint16_t*)y;
+    if (k == 1)
+        moe_combine_rows_kernel<1><<<grid, block, 0, stream>>>(rows, slot, topk_w, T, d, k, max_rows, out);
+    else if (k == 2)
+        moe_combine_rows_kernel<2><<<grid, block, 0, stream>>>(rows, slot, topk_w, T, d, k, max_rows, out);
+    else if (k <= 4)
+        moe_combine_rows_kernel<4><<<grid, block, 0, stream>>>(rows, slot, topk_w, T, d, k, max_rows, out);
+    else
+        moe_combine_rows_kernel<8><<<grid, block, 0, stream>>>(rows, slot, topk_w, T, d, k, max_rows, out);
+    return hipGetLastError();
 }
