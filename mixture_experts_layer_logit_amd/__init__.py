@@ -152,10 +152,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            torch.cuda.init()
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", None)
+            # the stream's handle without a Stream object around it, which takes
+            # longer to make than a small kernel to launch
+            _current_stream = (lambda: raw(device())) if raw and device else (
+                lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -321,14 +333,19 @@ def moe_backward(p, dy, x, Wg, W1, W2, logits, info, saved, dx, dWg, dbg, dW1, d
                                _ptr(dW1), _ptr(dW2), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
+_scale_types = {}
+
+
 def _scale_type(scales) -> int:
     """MOE_SCALE_* of a tensor of block scales, by its element type."""
-    import torch
-    if scales.dtype == torch.float32:
-        return MOE_SCALE_F32
-    if scales.dtype in (torch.uint8, torch.float8_e8m0fnu):
-        return MOE_SCALE_E8M0
-    raise TypeError(f"block scales are float32 or E8M0 (uint8 or float8_e8m0fnu), not {scales.dtype}")
+    if not _scale_types:
+        import torch
+        _scale_types.update({torch.float32: MOE_SCALE_F32, torch.uint8: MOE_SCALE_E8M0,
+                             torch.float8_e8m0fnu: MOE_SCALE_E8M0})
+    kind = _scale_types.get(scales.dtype)
+    if kind is None:
+        raise TypeError(f"block scales are float32 or E8M0 (uint8 or float8_e8m0fnu), not {scales.dtype}")
+    return kind
 
 
 def _e8m0(scales, name):

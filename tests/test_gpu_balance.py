@@ -48,7 +48,7 @@ def cuts(T, S, kind, g):
     (1, 1, 1, 1, "none"), (1, 8, 2, 1, "none"), (5, 2, 1, 5, "full"), (64, 8, 2, 1, "none"), (100, 7, 3, 4, "padded"),
     (257, 33, 2, 6, "late"), (300, 64, 8, 3, "full"), (1031, 65, 4, 9, "padded"), (500, 128, 1, 40, "padded"),
     (77, 160, 8, 2, "full"), (129, 256, 8, 3, "late"), (64, 500, 6, 2, "padded"), (65, 1024, 8, 3, "full"),
-    (9000, 16, 2, 3, "padded"), (40000, 8, 2, 5, "padded"), (700, 4, 1, 600, "full")])
+    (9000, 16, 2, 3, "padded"), (40000, 8, 2, 5, "padded"), (700, 4, 1, 600, "full"), (3000, 12, 2, 1500, "padded"), (2500, 512, 4, 2, "late")])
 def test_against_the_definition(T, E, k, S, kind, normalize, lam):
     print(f"[balance] T={T} E={E} k={k} S={S} {kind} normalize={normalize} lam={lam}", flush=True)
     g, z, idx = make(T, E, k)
@@ -207,3 +207,33 @@ def test_graph_replay_and_streams():
         graph.replay()
         for a, b in zip(take(), want):
             assert np.array_equal(a, b), f"replay {rep}"
+
+
+def test_tensors_that_start_inside_16_bytes():
+    """Rows of whole 16-byte pieces whose tensors do not start on one."""
+    T, E, k = 70, 16, 2
+    g, z, idx = make(T, E, k)
+    p = moe.problem(T, 64, E, k, 64)
+    zt = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+    zt.copy_(dev(z))
+    dz = torch.empty(T * E + 3, device="cuda")[3:].view(T, E)
+    counts = torch.empty(E + 1, dtype=torch.int32, device="cuda")[1:].view(1, E)
+    losses = torch.empty(2, device="cuda")
+    ws = torch.empty(moe.moe_balance_workspace_size(p, 1), dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(p, zt, dev(idx), None, counts, losses, dz, 0.5, 0.1, ws)
+    torch.cuda.synchronize()
+    c, l, want, bound = ref.balance(z, idx, np.array([0, T]), 0.5, 0.1)
+    assert np.array_equal(counts.cpu().numpy(), c) and np.all(np.abs(dz.cpu().numpy() - want) <= bound)
+
+
+def test_close_logits_under_the_normalisation():
+    """Logits a tiny step apart, on a large common offset and on none."""
+    T, E, k = 24, 8, 2
+    g, z, idx = make(T, E, k)
+    p = moe.problem(T, 64, E, k, 64, normalize=True)
+    for values in (1e-25 * z, 1024.0 + z * 2.0 ** -10):
+        values = values.astype(np.float32)
+        counts, losses, dz = call(p, values, idx, None, 0.5, 0.0)
+        c, l, want, bound = ref.balance(values, idx, np.array([0, T]), 0.5, 0.0, True)
+        assert np.all(np.abs(dz - want) <= bound)
+        assert abs(losses[0] - l[0]) <= 1e-5
