@@ -401,8 +401,10 @@ moe_status moe_forward_fp8(const moe_problem* p, const void* x, const void* Wg, 
  *     checkpoint's own scales); each block's product is scaled in fp32.
  * An E8M0 byte of 255 is NaN.  Requirements beyond the common limits:
  * problem->dtype == MOE_BF16, d and F multiples of 128.  Codes must be 16-byte
- * aligned, fp32 scales 4-byte, E8M0 scales need no alignment.  NaN and infinite
- * values to quantise violate a precondition. */
+ * aligned, fp32 scales 4-byte, E8M0 scales need no alignment.  A NaN
+ * to quantise becomes a NaN code and changes no other value of its block; an
+ * infinity becomes a NaN code and may make NaNs of other values of its block.
+ * Products with a NaN code are NaN, and so are the rows they end up in. */
 enum { MOE_SCALE_E8M0 = 0, MOE_SCALE_F32 = 1 };
 
 /* Quantise rows rows of K values (src_dtype MOE_F32 or MOE_BF16; K a multiple
@@ -471,7 +473,8 @@ moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void
  * p as in moe_route, after the optional normalisation (a token with equal
  * logits then has no gradient from aux).  Without the normalisation a logit of
  * -infinity (an expert closed to the token) has p = 0 and gradient 0, and a
- * token whose logits are all -infinity adds nothing to either loss.  T == 0
+ * token whose logits are all -infinity adds nothing to either loss.  A NaN
+ * logit makes its token's gradient and both losses NaN.  T == 0
  * clears counts and losses.  Probabilities in fp32, sums over tokens in fp64 in
  * fixed orders (the same bits on every run).  offsets outside [0, T] are
  * clamped.  Uses T, E, k, normalize and lambda of the problem; 1 <= n_seq <=

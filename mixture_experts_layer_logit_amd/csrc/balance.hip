@@ -22,14 +22,15 @@ namespace moe {
 // Work split: four launches.  One clears the counts and finds S+ and N.  One
 // counts: a block takes a run of tokens; a run inside one sequence is added in
 // an LDS histogram and flushed, one with a border in it goes to memory
-// directly, both with integer atomics, whose order does not change the counts.  One does the rest: G lanes take a token, lane l the values
-// 4 (l + G r) .. + 3 of its row, so a row is read and written in 16-byte
-// pieces and its sums stay in a few lanes (DPP steps up to 16 lanes); each
-// block adds its tokens' terms in fp64 in a fixed order.  A last launch adds
-// the blocks in a fixed order, so the sums have the same bits on every run (a
-// ticket by which the last block to finish would do that needs a release
-// fence in every block, which writes the gradients back from the XCDs' caches
-// first: 42 us against 7 us for 65536 tokens of 64 experts).
+// directly, both with integer atomics, whose order does not change the counts.
+// One does the rest: G lanes take a token, lane l the values 4 (l + G r) .. + 3
+// of its row, so a row is read and written in 16-byte pieces and its sums stay
+// in a few lanes (DPP steps up to 16 lanes); each block adds its tokens' terms
+// in fp64 in a fixed order.  A last launch adds the blocks in a fixed order, so
+// the sums have the same bits on every run (a ticket by which the last block to
+// finish would do that needs a release fence in every block, which writes the
+// gradients back from the XCDs' caches first: the launch took 42 us with it, 12
+// without, for 65536 tokens of 64 experts; the launch it spares takes 4).
 // A small batch takes one block that does all of it in one launch.
 constexpr int kBalanceBlocks = 2048;
 constexpr int kCountChunk = 256;      // tokens of a counting block
@@ -279,19 +280,19 @@ __device__ __forceinline__ void balance_tokens(const BalanceArgs& g, const Borde
             top = fmaxf(top, z[i]);
         }
         top = group_top<G>(top);
-        const bool any = top > -INFINITY;  // a row of -inf alone adds nothing
+        const bool any = top > -INFINITY;  // a row of -inf alone adds nothing, one of NaN and -inf is NaN
         float q[N], sum = 0.0f, m = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            z[i] = any ? z[i] - top : -INFINITY;
+            z[i] -= any ? top : 0.0f;
             q[i] = __builtin_amdgcn_exp2f(z[i] * kLog2e);
             sum += q[i];
             m += 4 * (li + G * (i / 4)) + i % 4 < E ? z[i] : 0.0f;
         }
         sum = group_sum<G>(sum);
         constexpr float kLn2 = 0.693147180559945309f;
-        const float lse = any ? top + __builtin_amdgcn_logf(sum) * kLn2 : 0.0f;
-        const float inv = any ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+        const float lse = any ? top + __builtin_amdgcn_logf(sum) * kLn2 : sum;  // sum: 0 or NaN
+        const float inv = any ? __builtin_amdgcn_rcpf(sum) : sum;
         float p[N], inner = 0.0f, c = 1.0f;
         if (g.normalize) {
             // the differences by a power of two near their mean's, so that the

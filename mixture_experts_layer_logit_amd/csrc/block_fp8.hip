@@ -243,7 +243,7 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
                 if constexpr (kGlu)
                     v[q] = glu(u, acc[j + kHalfF][4 * g4 + q]);
                 else if constexpr (EPI == BEPI_RELU)
-                    v[q] = fmaxf(u, 0.0f);
+                    v[q] = u <= 0.0f ? 0.0f : u;  // a NaN stays one
                 else
                     v[q] = u;
             }

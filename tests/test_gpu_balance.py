@@ -135,6 +135,37 @@ def test_masked_logits():
     assert np.all(np.abs(losses - l) <= 1e-4 * np.abs(l))
 
 
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("T", [40, 9000])
+def test_nan_logits_are_not_hidden(T, normalize):
+    """One NaN in a token, NaNs alone, NaNs beside -inf: NaN gradients of that
+    token and NaN losses; the other tokens' gradients are the clean ones."""
+    E, k = 9, 2
+    g, z, idx = make(T, E, k)
+    p = moe.problem(T, 64, E, k, 64, normalize=normalize)
+    clean = call(p, z, idx, None, 0.5, 0.2)
+    for t, values in ((3, [np.nan] + [0.5] * 8), (17, [np.nan] * 9), (T - 1, [-np.inf, np.nan] * 4 + [-np.inf])):
+        bad = z.copy()
+        bad[t] = values
+        counts, losses, dz = call(p, bad, idx, None, 0.5, 0.2)
+        others = np.arange(T) != t
+        assert np.array_equal(counts, clean[0]) and np.all(np.isnan(losses)) and np.all(np.isnan(dz[t]))
+        assert np.array_equal(dz[others], clean[2][others])
+
+
+@pytest.mark.parametrize("T", [40, 9000])
+def test_what_padding_holds_does_not_matter(T):
+    """NaN logits and any indices in the tokens of no sequence."""
+    E, k = 16, 2
+    g, z, idx = make(T, E, k)
+    off = np.array([3, T // 2, T - 7], np.int32)
+    p = moe.problem(T, 64, E, k, 64)
+    clean = call(p, z, idx, off, 0.5, 0.2)
+    z[:3], z[T - 7:], idx[:3], idx[T - 7:] = np.nan, np.nan, -5, 1 << 29
+    for a, b in zip(call(p, z, idx, off, 0.5, 0.2), clean):
+        assert np.array_equal(a, b)
+
+
 def test_equal_logits_under_the_normalisation():
     T, E, k = 12, 6, 2
     z = np.full((T, E), 3.25, np.float32)

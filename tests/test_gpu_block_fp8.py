@@ -187,6 +187,9 @@ class Case:
             v, dv = ref.product(self.h[r], self.w2[e])
             over = np.abs(y[r] - v) - (dv + ref.U8 * (np.abs(v) + dv))
             assert np.all(over <= 0), f"expert {e}: {over.max():.3e} beyond the bound"
+            # bf16 rounds evenly within half a step of at most U8 |v|: U8 / sqrt(3)
+            # = 0.577 U8 in the root mean square; the sums add about 2^-13.8
+            assert np.linalg.norm(y[r] - v) <= 0.6 * ref.U8 * np.linalg.norm(v), f"expert {e}: in the norm"
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
@@ -243,6 +246,50 @@ def test_scales_at_the_ends_of_their_range():
     for e in range(2):
         c.w1[e] = ref.widen_matrix(c.W1[e], np.exp2(c.s1[e].astype(np.float64) - 127))
     c.check_up(*c.up())
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_and_infinity_to_quantise(dtype, block_rows):
+    """A NaN becomes a NaN code and leaves its block as a zero would; an infinity
+    becomes a NaN code."""
+    rows, K = 140, 384
+    v = gen(5).standard_normal((rows, K)).astype(np.float32)
+    v[[2, 131], [7, 130]] = 0
+    bad = v.copy()
+    bad[2, 7], bad[131, 130] = np.nan, -np.nan
+    bad[9, 256:] = np.nan
+    v[9, 256:] = 0
+    out = []
+    for values in (v, bad, np.where(np.isnan(bad), np.inf, bad)):
+        src = bf16(values)[0] if dtype == "bf16" else dev(values)
+        codes = torch.full((rows, K), 0xA5, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(-(-rows // block_rows), K // BLK, dtype=torch.uint8, device="cuda")
+        moe.moe_quantize_fp8_block(src, codes, scales, block_rows=block_rows)
+        torch.cuda.synchronize()
+        out.append((codes.cpu().numpy(), scales.cpu().numpy()))
+    at = np.isnan(bad)
+    (c0, s0), (c1, s1), (c2, _) = out
+    assert np.array_equal(s1, s0) and np.array_equal(c1[~at], c0[~at])
+    assert np.all((c1[at] & 0x7F) == 0x7F) and np.all((c2[at] & 0x7F) == 0x7F)
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("shape", [(40, 256, 3, 2, 384, "relu", "even"), (40, 256, 3, 2, 384, "swiglu", "even"),
+                                   (600, 256, 2, 1, 384, "relu", "even"), (33, 2176, 5, 2, 384, "relu", "skew")],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_nan_codes_reach_their_rows_and_no_other(shape, f32):
+    c = Case(*shape, f32)
+    clean_h, clean_y = c.up(ws=c.workspace(0)), c.down(c.workspace(0))
+    tok = int(c.src[c.off[-1] // 2])
+    rows = np.zeros(c.T * c.k, bool)
+    rows[: c.off[-1]] = c.src[: c.off[-1]] == tok
+    c.xq[tok, 5] = 0x7F
+    c.hq[rows, 140] = 0xFF
+    (hq, hs), y = c.up(ws=c.workspace(0)), c.down(c.workspace(0))
+    assert np.all((hq[rows] & 0x7F) == 0x7F) and np.all(np.isnan(y[rows]))
+    assert np.array_equal(hq[~rows], clean_h[0][~rows]) and np.array_equal(hs[~rows], clean_h[1][~rows])
+    assert np.array_equal(y[~rows], clean_y[~rows])
 
 
 def test_strided_tensor_is_refused():
