@@ -63,11 +63,16 @@ def widen_matrix(codes, s):
 
 
 def product(a, w):
-    """a w^T in 64 bits, and a bound on an fp32 sum of it in any order: K + 8
-    roundings (K additions, the scales' products) of at most U24 of the sum of
-    magnitudes each."""
+    """a w^T in 64 bits, and a bound on what the FP8 matrix cores make of it.
+    The products of E4M3 codes (4 x 4 bits) are exact.  The cores add those of
+    neighbouring values on a grid of 2^-13 of the group's largest (measured for
+    gfx950): each group's sum is off by at most 2^-13 max |a w| <= 2^-13 times the
+    group's sum of |a w|, so all groups together by 2^-13 sum |a||w|.  The groups'
+    sums then take at most K fp32 additions and the scales' products, K + 8
+    roundings of at most U24 of the sum of magnitudes each.  (One product left
+    out of K <= 2304 even ones is 2^-11.2 of that sum.)"""
     K = a.shape[1]
-    return a @ w.T, (K + 8) * U24 * (np.abs(a) @ np.abs(w).T)
+    return a @ w.T, (2.0 ** -13 + (K + 8) * U24) * (np.abs(a) @ np.abs(w).T)
 
 
 def hidden(a, w, act, F):
