@@ -409,6 +409,8 @@ def moe_balance_loss(p, logits, topk_idx, seq_offsets, counts, losses, dlogits, 
     """counts [n_seq, E] int32, losses [2] = (aux, Z), dlogits [T, E] (or None) of
     the sequences seq_offsets [n_seq + 1] int32 (None: one sequence of all tokens)."""
     n_seq = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if seq_offsets is not None and seq_offsets.element_size() != 4:
+        raise TypeError(f"seq_offsets: int32, not {seq_offsets.dtype}")
     _check(load().moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
                                    float(aux_coef), float(z_coef), _ptr(counts), _ptr(losses), _ptr(dlogits),
                                    _ptr(ws), _nbytes(ws), _stream(stream)))

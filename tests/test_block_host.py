@@ -174,6 +174,13 @@ def test_balance_refusals(kw, want):
     assert moe.load().moe_last_error()
 
 
+def test_binding_checks_the_offsets_type():
+    torch = pytest.importorskip("torch")
+    f, i = torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        moe.moe_balance_loss(prob(), f, f, i, f, f, None, stream=0)
+
+
 def test_balance_counts_beyond_32_bits_are_refused():
     n = ctypes.c_size_t()
     assert status("moe_balance_workspace_size", ctypes.byref(prob(E=1024, k=2)), 1 << 21, ctypes.byref(n)) == 2
