@@ -333,15 +333,20 @@ def moe_backward(p, dy, x, Wg, W1, W2, logits, info, saved, dx, dWg, dbg, dW1, d
                                _ptr(dW1), _ptr(dW2), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
-_scale_types = {}
+_scale_types, _src_types = {}, {}
+
+
+def _fill_types():
+    import torch
+    _scale_types.update({torch.float32: MOE_SCALE_F32, torch.uint8: MOE_SCALE_E8M0,
+                         torch.float8_e8m0fnu: MOE_SCALE_E8M0})
+    _src_types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
 
 
 def _scale_type(scales) -> int:
     """MOE_SCALE_* of a tensor of block scales, by its element type."""
     if not _scale_types:
-        import torch
-        _scale_types.update({torch.float32: MOE_SCALE_F32, torch.uint8: MOE_SCALE_E8M0,
-                             torch.float8_e8m0fnu: MOE_SCALE_E8M0})
+        _fill_types()
     kind = _scale_types.get(scales.dtype)
     if kind is None:
         raise TypeError(f"block scales are float32 or E8M0 (uint8 or float8_e8m0fnu), not {scales.dtype}")
@@ -358,12 +363,13 @@ def moe_quantize_fp8_block(src, codes, scales, block_rows=1, stream=None):
     """Rows of src (fp32 or bf16 tensor [rows, K]) to E4M3 codes (uint8 [rows, K])
     with a power-of-two scale per block of block_rows (1 or 128) x 128 values;
     scales [ceil(rows / block_rows), K / 128] is uint8 / float8_e8m0fnu (E8M0) or fp32."""
-    import torch
-    dt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}[src.dtype]
+    kind = _scale_type(scales)
+    dt = _src_types.get(src.dtype)
+    if dt is None:
+        raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
     K = src.shape[-1]
-    rows = src.numel() // max(K, 1)
-    _check(load().moe_quantize_fp8_block(_ptr(src), dt, rows, K, int(block_rows), _ptr(codes), _ptr(scales),
-                                         _scale_type(scales), _stream(stream)))
+    _check(load().moe_quantize_fp8_block(_ptr(src), dt, src.numel() // (K or 1), K, block_rows, _ptr(codes),
+                                         _ptr(scales), kind, _stream(stream)))
 
 
 def moe_fp8_block_workspace_size(p) -> int:

@@ -109,8 +109,8 @@ __global__ __launch_bounds__(256) void moe_quantize_tiles_kernel(const typename 
 }
 
 // ---------------------------------------------------------------- grouped GEMM
-// Rows of expert e's segment times its weight matrix.  Block tile BM x 256,
-// WM x WN wavefronts, K in slices of 128 values (one scale block), each slice
+// Rows of expert e's segment times its weight matrix.  Block tile BM x BN (256
+// weight rows; 128, where a half is 64, for few tiles), WM x WN wavefronts, K in slices of 128 values (one scale block), each slice
 // loaded from memory straight into one of S LDS stages.  The 256 weight rows
 // of a tile are two halves of 128: for SwiGLU the gate rows and the matching
 // up rows of 128 hidden columns, else 256 consecutive rows; each half lies in
@@ -130,16 +130,22 @@ constexpr int kBlkSplitSlots = 256;  // partial tiles the workspace holds
 constexpr int kBlkMinPart = 4;       // K slices of a part
 [[maybe_unused]] constexpr int kBlkMaxSlices = 512;   // K <= 65536
 
-template <int BM_, int WM_, int WN_, int S_, int GM_>
+template <int BM_, int WM_, int WN_, int S_, int GM_, int BN_ = 256, int PER_CU_ = 1>
 struct BlockShape {
-    static constexpr int BM = BM_, BN = 256, WM = WM_, WN = WN_, S = S_, GM = GM_, RB = 128;
+    static constexpr int BM = BM_, BN = BN_, kHalf = BN / 2, kPerCu = PER_CU_;
+    static constexpr int WM = WM_, WN = WN_, S = S_, GM = GM_, RB = 128;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
-    static constexpr int kWavesPerSimd = kWaves / 4;
+    static constexpr int kWavesPerSimd = kWaves / 4 * kPerCu;
     static constexpr int kWaveM = BM / WM, kWaveN = BN / WN;
     static constexpr int kFM = kWaveM / 32, kFN = kWaveN / 32;
     static constexpr int kRows = 1024 / RB;  // tile rows of a 1 KB load
     static constexpr int kLdsA = BM * RB, kLdsW = BN * RB;
-    static constexpr int kScl = kThreads * 4;  // scales of the stage's activation rows, a dword each
+    // Scales of the stage's activation rows, a dword each.  Each wavefront loads 64
+    // rows' (none behind row BM); where two blocks have to fit a CU, the others
+    // load the same rows' into the same place (as the 256-row tile's second four
+    // wavefronts that would cost 4 %).
+    static constexpr int kSclWaves = kPerCu > 1 ? BM / kWave : kWaves;
+    static constexpr int kScl = kSclWaves * kWave * 4;
     static constexpr int kStage = kLdsA + kLdsW + kScl;
     static constexpr int kBlkA = BM / kRows / kWaves, kBlkW = BN / kRows / kWaves;  // loads per wavefront and stage
     static constexpr int kLoads = kBlkA + kBlkW + 1;
@@ -220,7 +226,8 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
 {
     constexpr bool kGlu = EPI == BEPI_SWIGLU;
     constexpr bool kRows32 = EPI == BEPI_F32, kPlain = EPI == BEPI_NONE || kRows32;
-    constexpr int HC = kGlu ? 128 : 256;  // output columns of the tile
+    static_assert(S::BN == 256 || !kGlu, "h is stored by whole blocks");
+    constexpr int HC = kGlu ? 128 : S::BN;  // output columns of the tile
     constexpr int kRows = S::WM * 32;
     constexpr int kEl = EPI == BEPI_NONE ? 2 : 4;
     constexpr int kRowBytes = HC * kEl;
@@ -235,7 +242,7 @@ __device__ __forceinline__ void block_store(const f32x16 (&acc)[S::kFN], int i, 
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
             constexpr int kHalfN = S::kWaveN / 2, kHalfF = S::kFN / 2;
-            const int col = (j / kHalfF) * 128 + wn * kHalfN + (j % kHalfF) * 32 + 8 * g4 + 4 * (lane >> 5);
+            const int col = (j / kHalfF) * S::kHalf + wn * kHalfN + (j % kHalfF) * 32 + 8 * g4 + 4 * (lane >> 5);
             float v[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -310,7 +317,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body uses device-only types; the host pass needs the stub only
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
-    __shared__ uint32_t s_ws[2][kBlkMaxSlices];  // the tile's weight scales
+    __shared__ uint32_t s_ws[S::BN / kBlk][kBlkMaxSlices];  // the tile's weight scales
     __shared__ int32_t s_pref[kGemmMaxE + 1];
     __shared__ int32_t s_wsum[S::kWaves];
     const int tid = threadIdx.x;
@@ -327,7 +334,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
     const uint32_t rdW = S::kLdsA + bswz<S>(wn * kHalfN + (lane & 31), 2 * (lane >> 5));
     const uint32_t rdS = S::kLdsA + S::kLdsW + 4 * (wm * S::kWaveM + (lane & 31));
 
-    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : S::BN;
     const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
     tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
     const int total = s_pref[g.E];
@@ -339,8 +346,12 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
 
     for (int base = 0; base < items; base += G) {
         const int b = blockIdx.x;
-        const int item = (G % 8 == 0) ? base + (b % 8) * (G / 8) + b / 8 : base + b;  // an XCD's blocks side by side
-        if (item >= items)
+        // an XCD's blocks side by side; with two blocks a CU a round that is not
+        // full is spread over all XCDs (half a round 39.5 -> 25.7 us; with one block
+        // a CU no difference, and scalar registers that the 256-row tile lacks)
+        const int each = S::kPerCu > 1 ? (min(G, items - base) + 7) / 8 : G / 8;
+        const int item = (G % 8 == 0) ? base + (b % 8) * each + b / 8 : base + b;
+        if (item >= items || (S::kPerCu > 1 && G % 8 == 0 && b / 8 >= each))
             continue;
         int tile = item, k0 = 0, k1 = nk, slot = -1;
         if (item >= full) {
@@ -360,7 +371,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         const uint32_t lchunk = (uint32_t)((lane % kCh) ^ bswz_term<S>(lrow)) * 16;
         i32x4 rsA, rsS;
         uint32_t voffA[S::kBlkA], voffS;
-        const int srow = wave * kWave + lane;  // the tile row whose scale this lane loads
+        const int srow = wave % S::kSclWaves * kWave + lane;  // the tile row whose scale this lane loads
         if (g.gather) {
             rsA = make_rsrc(g.A, (uint32_t)g.gather_rows * (uint32_t)K);
             rsS = make_rsrc(g.As, (uint32_t)g.gather_rows * (uint32_t)nk);
@@ -387,7 +398,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         // the second half of the last tile may lie behind the matrix
         const i32x4 rsW = make_rsrc(g.W + (size_t)t.e * g.Nw * K, (uint32_t)g.Nw * (uint32_t)K);
         const uint32_t voffW = (uint32_t)lrow * (uint32_t)K + lchunk;
-        const uint32_t half1 = EPI == BEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + 128);
+        const uint32_t half1 = EPI == BEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + S::kHalf);
         const bool second = EPI == BEPI_SWIGLU || (int)half1 < g.Nw;
         const uint32_t voffW1 = second ? voffW : 0xf0000000u, row0 = (uint32_t)t.n0 * (uint32_t)K;
         const uint32_t row1 = second ? half1 * (uint32_t)K : 0, step = S::kRows * S::kWaves * (uint32_t)K;
@@ -425,7 +436,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                     dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == BEPI_SWIGLU ? voffW : voffW1,
                           soff + row1 + (p - S::kBlkW / 2) * step);
                 else if (p == S::kBlkW)
-                    dma_byte(rsS, at + S::kLdsA + S::kLdsW + wave * 256, voffS, kb);
+                    dma_byte(rsS, at + S::kLdsA + S::kLdsW + wave % S::kSclWaves * 256, voffS, kb);
                 else
                     dma16(rsA, dst + S::kWaves * (p - S::kBlkW - 1) * 1024, voffA[p > S::kBlkW ? p - S::kBlkW - 1 : 0],
                           soff);
@@ -434,8 +445,8 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
         auto load_weight_scales = [&]() {
             const size_t brow = (size_t)t.e * (g.Nw / kBlk);
             const int c0 = t.n0 / kBlk;
-            const int c1 = EPI == BEPI_SWIGLU ? (g.F + t.n0) / kBlk : min(c0 + 1, g.Nw / kBlk - 1);
-            for (int q = tid; q < 2 * (k1 - k0); q += S::kThreads) {
+            const int c1 = EPI == BEPI_SWIGLU ? (g.F + t.n0) / kBlk : min((t.n0 + S::kHalf) / kBlk, g.Nw / kBlk - 1);
+            for (int q = tid; q < S::BN / kBlk * (k1 - k0); q += S::kThreads) {
                 const int h = q >= k1 - k0, kb = k0 + q - (h ? k1 - k0 : 0);
                 const size_t at = (brow + (h ? c1 : c0)) * nk + kb;
                 if constexpr (WF32)
@@ -493,7 +504,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                 const int n = r / 2, h = r % 2;  // fragment, 16-byte half
                 const uint32_t x = (uint32_t)(kk * 64) ^ (uint32_t)(h * 16);
                 const i32x4 v = *reinterpret_cast<const i32x4*>(
-                    lds + st + (n < S::kFN ? (rdW ^ x) + ((n / kHalfF) * 128 + (n % kHalfF) * 32) * S::RB
+                    lds + st + (n < S::kFN ? (rdW ^ x) + ((n / kHalfF) * S::kHalf + (n % kHalfF) * 32) * S::RB
                                            : (rdA ^ x) + (n - S::kFN) * 32 * S::RB));
                 i32x8& dst = n < S::kFN ? nx.w[n] : nx.a[n - S::kFN];
                 if (h)
@@ -566,7 +577,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
             // in the order of the loop's own reads: the waits at its head are the
             // stricter of the two
             sw[0] = s_ws[0][slice_of(k0)];
-            sw[1] = s_ws[1][slice_of(k0)];
+            sw[1] = s_ws[S::BN / kBlk - 1][slice_of(k0)];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -589,7 +600,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
                 lds_barrier();
                 const int sn = slice_of(min(kt + 1, k1 - 1));
                 swn[0] = s_ws[0][sn];
-                swn[1] = s_ws[1][sn];
+                swn[1] = s_ws[S::BN / kBlk - 1][sn];
                 kstep(f1, f0, nxt * S::kStage, 0, yes, loads, kt + S::S, cur);
                 sw[0] = swn[0];
                 sw[1] = swn[1];
@@ -619,7 +630,7 @@ void moe_block_gemm_kernel(BlockGemmArgs g)
 #pragma unroll
             for (int i = 0; i < S::kFM; ++i)
                 if (i * 32 < t.rows)
-                    block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * 1024), g);
+                    block_store<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * S::BN * 4), g);
         } else {
             // rows past the segment's end stay unwritten
             float* dst = g.partial + (size_t)slot * S::kTileFloats;
@@ -645,11 +656,11 @@ template <typename S, int EPI>
 __global__ __launch_bounds__(S::kThreads) void moe_block_tail_kernel(BlockGemmArgs g, int G)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) uint8_t buf[S::WM * 32 * 1024];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf[S::WM * 32 * S::BN * 4];
     __shared__ int32_t s_pref[kGemmMaxE + 1];
     __shared__ int32_t s_wsum[S::kWaves];
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : S::BN;
     const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
     tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
     const int total = s_pref[g.E];
@@ -749,34 +760,56 @@ using namespace moe;
 // rows each: 13 / 14 us against 16 / 16).  fp32 weight scales need a product of
 // their own for each block before it is added, registers that the 256-row tile
 // does not have: 128 rows there.  32-row tiles and weights loaded straight into
-// the operands' registers, without LDS, were slower or equal at every size.
+// the operands' registers, without LDS, were slower or equal at every size (32-row
+// tiles also with two blocks a CU).
+//
+// Where 64 x 128 tiles are few, NarrowShape: two blocks a CU hide each other's
+// waits.  Not for SwiGLU, whose tile has to hold a block of 128 hidden columns of
+// both halves.  Down, E8M0 / fp32 scales, us, against the shapes above:
+//   tiles  rows     K        above        64 x 128
+//      64   256  1024   15.6 / 13.4     7.1 /  8.6
+//     128  1024  4096   37.6 / 30.0    18.0 / 20.8
+//     256     8 14336   88.3 / 89.1    81.5 / 82.3
+//     256    75  2048   18.9 / 22.5    11.9 / 14.2
+//     256   256  4096   34.1 / 29.3    28.6 / 29.8
+//     512     1   512    9.9 / 10.9     8.8 /  9.4
+//     512    75  1024   13.0 / 16.6    12.5 / 13.1
+//     512    25  2048   27.7 / 28.3    29.2 / 29.6
+//     512    75  4096   35.5 / 43.9    40.6 / 41.7
+//     512  2048  4096   39.2 / 35.6    29.1 / 31.0
+//    1024   256  1024   21.8 / 29.3    23.7 / 26.6
+// so up to a tile a CU, and up to two where K is below 2048 or the choice would be
+// the 256-row tile.
 typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
 typedef BlockShape<128, 2, 4, 3, 8> LargeF32Shape;
 typedef BlockShape<96, 1, 4, 3, 4> MediumShape;
 typedef BlockShape<64, 1, 4, 3, 4> SmallShape;
+typedef BlockShape<64, 2, 2, 3, 4, 128, 2> NarrowShape;
 constexpr int kLargeRows = 192;
 
-// Whether the last round is split along K.  The split costs a second launch
-// (about 4 us), so it is left out where K is short, and where the tiles expected
-// (rows spread evenly over min(rows, E) experts) fill more than half of the only
-// round: one token of two experts, 224 tiles of 256 CUs, 54.9 -> 51.8 us without.
+// Whether the last round (at most kBlkSplitSlots / 2 tiles of it) is split along K.
+// The split costs a second launch (about 4 us), so it is left out where K is short,
+// and where the tiles expected (rows spread evenly over min(rows, E) experts) fill
+// more than half of the only round: one token of two experts, 224 tiles of 256 CUs,
+// 54.9 -> 51.8 us without.
 template <typename S>
-bool split_pays(const BlockGemmArgs& g, long long ntn, int ncu)
+bool split_pays(const BlockGemmArgs& g, long long ntn, int blocks)
 {
     if (g.K < 2048)
         return false;
     const long long busy = std::min(g.E, g.max_rows);
     const long long tiles = busy * std::max(1ll, (g.max_rows / busy + S::BM - 1) / S::BM) * ntn;
-    return tiles <= ncu / 2 || tiles > ncu;
+    return tiles <= std::min(blocks, kBlkSplitSlots) / 2 || tiles > blocks;
 }
 
 template <typename S, int EPI, bool WF32>
 hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
 {
-    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : 256;
+    const int tile_cols = EPI == BEPI_SWIGLU ? 128 : S::BN;
     const long long ntn = (g.Nout + tile_cols - 1) / tile_cols;
     // upper bound on m-tiles: whole tiles plus one partial per expert
     const long long mt = g.max_rows / S::BM + (long long)std::min(g.E, g.max_rows);
+    ncu *= S::kPerCu;
     if (!split_pays<S>(g, ntn, ncu))
         g.partial = nullptr;
     long long grid = ncu;
@@ -792,15 +825,19 @@ hipError_t launch_shape(BlockGemmArgs g, int ncu, hipStream_t stream)
 }
 
 template <typename S, bool WF32>
-hipError_t launch_epi(int epi, const BlockGemmArgs& g, int ncu, hipStream_t s)
+hipError_t launch_narrow(int epi, const BlockGemmArgs& g, int ncu, hipStream_t s)
 {
     if (epi == BEPI_RELU)
         return launch_shape<S, BEPI_RELU, WF32>(g, ncu, s);
+    return epi == BEPI_F32 ? launch_shape<S, BEPI_F32, WF32>(g, ncu, s) : launch_shape<S, BEPI_NONE, WF32>(g, ncu, s);
+}
+
+template <typename S, bool WF32>
+hipError_t launch_epi(int epi, const BlockGemmArgs& g, int ncu, hipStream_t s)
+{
     if (epi == BEPI_SWIGLU)
         return launch_shape<S, BEPI_SWIGLU, WF32>(g, ncu, s);
-    if (epi == BEPI_F32)
-        return launch_shape<S, BEPI_F32, WF32>(g, ncu, s);
-    return launch_shape<S, BEPI_NONE, WF32>(g, ncu, s);
+    return launch_narrow<S, WF32>(epi, g, ncu, s);
 }
 
 template <typename ET, bool F32>
@@ -859,6 +896,10 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
 {
     const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F,
                              max_rows, partial};
+    const long long narrow = (long long)std::min(E, max_rows) * std::max(1, (mean_rows + 63) / 64) * (Nout / 128);
+    if (epi != BEPI_SWIGLU && narrow <= (K < 2048 || mean_rows >= kLargeRows ? 2 * ncu : ncu))
+        return wf32 ? launch_narrow<NarrowShape, true>(epi, g, ncu, stream)
+                    : launch_narrow<NarrowShape, false>(epi, g, ncu, stream);
     if (mean_rows >= kLargeRows)
         return wf32 ? launch_epi<LargeF32Shape, true>(epi, g, ncu, stream)
                     : launch_epi<LargeShape, false>(epi, g, ncu, stream);

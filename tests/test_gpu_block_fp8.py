@@ -129,6 +129,18 @@ SHAPES = [
     (513, 384, 3, 2, 640, "relu", "skew"),
     (700, 256, 2, 1, 512, "swiglu", "one"),
     (260, 2304, 2, 2, 2176, "swiglu", "skew"),
+    # ReLU and the down projection on few tiles (64 x 128), with a K split and
+    # several tiles a segment; then too many of those: 64, 96 and 256 rows (up,
+    # then down), and the last with a K split
+    (40, 2304, 3, 2, 384, "relu", "even"),
+    (400, 256, 3, 2, 1152, "relu", "skew"),
+    (1400, 128, 20, 1, 2560, "relu", "even"),
+    (1400, 2560, 20, 1, 128, "relu", "even"),
+    (2100, 128, 30, 1, 2560, "relu", "skew"),
+    (2100, 2560, 30, 1, 128, "swiglu", "even"),
+    (600, 128, 3, 1, 5632, "relu", "even"),
+    (600, 5632, 3, 1, 128, "relu", "skew"),
+    (2100, 2048, 1, 1, 2048, "relu", "even"),
 ]
 
 
