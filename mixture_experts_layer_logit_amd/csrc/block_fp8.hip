@@ -755,7 +755,11 @@ using namespace moe;
 //    160       173 / 89   144 / 76    152 / 80    148 / 79
 //    256       255 / 131  199 / 101   187 / 106   179 / 112
 //    512       456 / 221  355 / 177   323 / 165   270 / 148
-// The 96-row tile below 192 rows, the 256-row one from there on; where 96-row
+// The 96-row tile below 192 rows, the 256-row one from there on, but the 96-row or
+// else the 128-row one where all of its tiles, however the rows are spread, find
+// a CU each (SwiGLU, one expert of 2048 rows, 2048 x 1024: 16 us against 35; 4 of
+// 256, 2048 x 2048: 19 against 34; plain, one of 4096, 2048 x 2048: 22 with 128
+// rows against 41; spread over two rounds they lose up to 19 %).  Where 96-row
 // tiles leave CUs without one, the 64-row tile (16 experts, ReLU 1024 x 2048, 88
 // rows each: 13 / 14 us against 16 / 16).  fp32 weight scales need a product of
 // their own for each block before it is added, registers that the 256-row tile
@@ -781,7 +785,7 @@ using namespace moe;
 // so up to a tile a CU, and up to two where K is below 2048 or the choice would be
 // the 256-row tile.
 typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
-typedef BlockShape<128, 2, 4, 3, 8> LargeF32Shape;
+typedef BlockShape<128, 2, 4, 3, 8> Shape128;
 typedef BlockShape<96, 1, 4, 3, 4> MediumShape;
 typedef BlockShape<64, 1, 4, 3, 4> SmallShape;
 typedef BlockShape<64, 2, 2, 3, 4, 128, 2> NarrowShape;
@@ -900,12 +904,19 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
     if (epi != BEPI_SWIGLU && narrow <= (K < 2048 || mean_rows >= kLargeRows ? 2 * ncu : ncu))
         return wf32 ? launch_narrow<NarrowShape, true>(epi, g, ncu, stream)
                     : launch_narrow<NarrowShape, false>(epi, g, ncu, stream);
-    if (mean_rows >= kLargeRows)
-        return wf32 ? launch_epi<LargeF32Shape, true>(epi, g, ncu, stream)
-                    : launch_epi<LargeShape, false>(epi, g, ncu, stream);
     const int tile_cols = epi == BEPI_SWIGLU ? 128 : 256;
-    const long long tiles = (long long)std::min(E, max_rows) * ((mean_rows + 95) / 96 + (mean_rows == 0)) *
-                            ((Nout + tile_cols - 1) / tile_cols);
+    const long long ntn = (Nout + tile_cols - 1) / tile_cols, busy = std::min(E, max_rows);
+    if (mean_rows >= kLargeRows) {
+        auto most = [&](int bm) { return (busy == 1 ? (max_rows + bm - 1) / bm : max_rows / bm + busy) * ntn; };
+        if (wf32)
+            return launch_epi<Shape128, true>(epi, g, ncu, stream);
+        if (most(MediumShape::BM) <= ncu)
+            return launch_epi<MediumShape, false>(epi, g, ncu, stream);
+        if (most(Shape128::BM) <= ncu)
+            return launch_epi<Shape128, false>(epi, g, ncu, stream);
+        return launch_epi<LargeShape, false>(epi, g, ncu, stream);
+    }
+    const long long tiles = busy * ((mean_rows + 95) / 96 + (mean_rows == 0)) * ntn;
     if (tiles < ncu)
         return wf32 ? launch_epi<SmallShape, true>(epi, g, ncu, stream)
                     : launch_epi<SmallShape, false>(epi, g, ncu, stream);

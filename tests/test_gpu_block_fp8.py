@@ -130,8 +130,8 @@ SHAPES = [
     (700, 256, 2, 1, 512, "swiglu", "one"),
     (260, 2304, 2, 2, 2176, "swiglu", "skew"),
     # ReLU and the down projection on few tiles (64 x 128), with a K split and
-    # several tiles a segment; then too many of those: 64, 96 and 256 rows (up,
-    # then down), and the last with a K split
+    # several tiles a segment; then too many of those: 64 rows, 96, 96 although
+    # there are many, 128 and 256 (up or down); 256 rows with a K split
     (40, 2304, 3, 2, 384, "relu", "even"),
     (400, 256, 3, 2, 1152, "relu", "skew"),
     (1400, 128, 20, 1, 2560, "relu", "even"),
@@ -140,7 +140,13 @@ SHAPES = [
     (2100, 2560, 30, 1, 128, "swiglu", "even"),
     (600, 128, 3, 1, 5632, "relu", "even"),
     (600, 5632, 3, 1, 128, "relu", "skew"),
+    (1280, 128, 1, 1, 2560, "swiglu", "even"),
+    (1280, 5120, 1, 1, 128, "relu", "even"),
+    (1500, 128, 3, 1, 5632, "relu", "even"),
+    (1500, 5632, 3, 1, 128, "relu", "skew"),
+    (1500, 128, 3, 1, 2560, "swiglu", "skew"),
     (2100, 2048, 1, 1, 2048, "relu", "even"),
+    (2200, 2048, 1, 1, 4096, "swiglu", "even"),
 ]
 
 
