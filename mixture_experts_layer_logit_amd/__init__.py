@@ -368,7 +368,7 @@ def moe_quantize_fp8_block(src, codes, scales, block_rows=1, stream=None):
     if dt is None:
         raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
     K = src.shape[-1]
-    _check(load().moe_quantize_fp8_block(_ptr(src), dt, src.numel() // (K or 1), K, block_rows, _ptr(codes),
+    _check(load().moe_quantize_fp8_block(_ptr(src), dt, src.numel() // (K or 1), K, int(block_rows), _ptr(codes),
                                          _ptr(scales), kind, _stream(stream)))
 
 

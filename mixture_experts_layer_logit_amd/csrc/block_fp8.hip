@@ -109,14 +109,14 @@ __global__ __launch_bounds__(256) void moe_quantize_tiles_kernel(const typename 
 }
 
 // ---------------------------------------------------------------- grouped GEMM
-// Rows of expert e's segment times its weight matrix.  Block tile BM x BN (256
-// weight rows; 128, where a half is 64, for few tiles), WM x WN wavefronts, K in slices of 128 values (one scale block), each slice
-// loaded from memory straight into one of S LDS stages.  The 256 weight rows
-// of a tile are two halves of 128: for SwiGLU the gate rows and the matching
-// up rows of 128 hidden columns, else 256 consecutive rows; each half lies in
-// one row of weight blocks, so a tile has two weight scales per slice.  A
-// wavefront takes the same rows of both halves, so the gate and up values of
-// a hidden column meet in one lane.
+// Rows of expert e's segment times its weight matrix.  Block tile BM x BN, WM x WN
+// wavefronts, K in slices of 128 values (one scale block), each slice loaded from
+// memory straight into one of S LDS stages.  The 256 weight rows of a tile are two
+// halves of 128: for SwiGLU the gate rows and the matching up rows of 128 hidden
+// columns, else 256 consecutive rows; each half lies in one row of weight blocks,
+// so a tile has two weight scales per slice.  A wavefront takes the same rows of
+// both halves, so the gate and up values of a hidden column meet in one lane.
+// (Where tiles are few, 128 weight rows, two halves of 64 under one scale.)
 //
 // MFMA 32x32x64 f8f6f4 with block scales: lane l holds 32 consecutive K
 // values of operand row l % 32 (the half l / 32 of the 64) and the E8M0 byte
@@ -782,8 +782,13 @@ using namespace moe;
 //     512    75  4096   35.5 / 43.9    40.6 / 41.7
 //     512  2048  4096   39.2 / 35.6    29.1 / 31.0
 //    1024   256  1024   21.8 / 29.3    23.7 / 26.6
-// so up to a tile a CU, and up to two where K is below 2048 or the choice would be
-// the 256-row tile.
+//    2048     8  1024   56.9 / 58.8    54.0 / 53.9
+//    2048    32  1024   62.2 / 65.4    58.7 / 57.9
+//    2048    64  1024   69.3 / 76.3    72.6 / 70.9
+//    2048   128  1024   45.9 / 69.8    50.5 / 52.1
+// so (narrow_pays) up to a tile a CU; up to two where K is below 2048, where the
+// choice would be the 256-row tile, or with fp32 scales from 64 rows on; and any
+// number for K below 2048 with fp32 scales or few rows.
 typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
 typedef BlockShape<128, 2, 4, 3, 8> Shape128;
 typedef BlockShape<96, 1, 4, 3, 4> MediumShape;
@@ -804,6 +809,17 @@ bool split_pays(const BlockGemmArgs& g, long long ntn, int blocks)
     const long long busy = std::min(g.E, g.max_rows);
     const long long tiles = busy * std::max(1ll, (g.max_rows / busy + S::BM - 1) / S::BM) * ntn;
     return tiles <= std::min(blocks, kBlkSplitSlots) / 2 || tiles > blocks;
+}
+
+bool narrow_pays(int mean_rows, long long tiles, int K, bool wf32, int ncu)
+{
+    if (tiles <= ncu)
+        return true;
+    if (mean_rows >= kLargeRows)
+        return tiles <= 2 * ncu;
+    if (K < 2048)
+        return wf32 || mean_rows <= 32 || tiles <= 2 * ncu;
+    return wf32 && mean_rows >= 64 && tiles <= 2 * ncu;
 }
 
 template <typename S, int EPI, bool WF32>
@@ -901,7 +917,7 @@ extern "C" hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A,
     const BlockGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F,
                              max_rows, partial};
     const long long narrow = (long long)std::min(E, max_rows) * std::max(1, (mean_rows + 63) / 64) * (Nout / 128);
-    if (epi != BEPI_SWIGLU && narrow <= (K < 2048 || mean_rows >= kLargeRows ? 2 * ncu : ncu))
+    if (epi != BEPI_SWIGLU && narrow_pays(mean_rows, narrow, K, wf32, ncu))
         return wf32 ? launch_narrow<NarrowShape, true>(epi, g, ncu, stream)
                     : launch_narrow<NarrowShape, false>(epi, g, ncu, stream);
     const int tile_cols = epi == BEPI_SWIGLU ? 128 : 256;

@@ -233,6 +233,25 @@ def test_down(shape, f32):
     assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("d", [22016, 32768])
+def test_down_with_fp32_scales_on_many_columns(d):
+    """fp32 scales from K 2048 on with more than two 64 x 128 tiles a CU: 64 rows
+    and 96."""
+    T, F = 130, 2048
+    g = gen(d)
+    hq, he = ref.quantise(g.standard_normal((T, F)))
+    w = g.integers(0, 0x60, (1, d, F)).astype(np.uint8) | g.integers(0, 2, (1, d, F)).astype(np.uint8) << 7
+    s = (0.01 * (0.5 + g.random((1, d // BLK, F // BLK)))).astype(np.float32)
+    y = torch.full((T, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_down_fp8_block(moe.problem(T, d, 1, 1, F), dev(hq), dev((he + 127).astype(np.uint8)),
+                                  dev(np.array([0, T], np.int32)), dev(w), dev(s), y)
+    torch.cuda.synchronize()
+    v, dv = ref.product(ref.widen_rows(hq, he), ref.widen_matrix(w[0], s[0]))
+    y = y.double().cpu().numpy()
+    assert np.all(np.abs(y - v) <= dv + ref.U8 * (np.abs(v) + dv))
+    assert np.linalg.norm(y - v) <= 0.6 * ref.U8 * np.linalg.norm(v)
+
+
 def test_rows_behind_the_last_segment_stay():
     c = Case(200, 256, 4, 2, 384, "swiglu", "even", False)
     c.off = np.minimum(c.off, 333).astype(np.int32)  # the capacity clip leaves fewer than T*k rows
