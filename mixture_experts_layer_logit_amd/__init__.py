@@ -334,13 +334,31 @@ def moe_backward(p, dy, x, Wg, W1, W2, logits, info, saved, dx, dWg, dbg, dW1, d
 
 
 _scale_types, _src_types = {}, {}
+_f32 = _i32 = None
 
 
 def _fill_types():
     import torch
+    global _f32, _i32
+    _f32, _i32 = torch.float32, torch.int32
     _scale_types.update({torch.float32: MOE_SCALE_F32, torch.uint8: MOE_SCALE_E8M0,
                          torch.float8_e8m0fnu: MOE_SCALE_E8M0})
     _src_types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
+
+
+def _refuse(types, sizes):
+    """TypeError for the first (name, tensor, type) whose tensor has another element
+    type, ValueError for the first (name, tensor, least) with fewer elements: the
+    kernels would read the bytes as something else, or go past their end."""
+    def tensor(t):
+        return t is not None and not isinstance(t, int)  # plain addresses pass
+
+    for name, t, kind in types:
+        if tensor(t) and t.dtype is not kind:
+            raise TypeError(f"{name}: {kind}, not {t.dtype}")
+    for name, t, least in sizes:
+        if tensor(t) and t.numel() < least:
+            raise ValueError(f"{name}: {t.numel()} elements, {least} are needed")
 
 
 def _scale_type(scales) -> int:
@@ -413,10 +431,26 @@ def moe_balance_workspace_size(p, n_seq) -> int:
 def moe_balance_loss(p, logits, topk_idx, seq_offsets, counts, losses, dlogits, aux_coef=0.0, z_coef=0.0, ws=None,
                      stream=None):
     """counts [n_seq, E] int32, losses [2] = (aux, Z), dlogits [T, E] (or None) of
-    the sequences seq_offsets [n_seq + 1] int32 (None: one sequence of all tokens)."""
-    n_seq = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    if seq_offsets is not None and seq_offsets.element_size() != 4:
-        raise TypeError(f"seq_offsets: int32, not {seq_offsets.dtype}")
+    the sequences seq_offsets [n_seq + 1] int32 (None: one sequence of all tokens).
+    logits [T, E], losses and dlogits are float32, topk_idx [T, k] int32: other types
+    raise TypeError, tensors with too few elements ValueError."""
+    if _f32 is None:
+        _fill_types()
+    n_seq, E, T = 1 if seq_offsets is None else seq_offsets.numel() - 1, p.E, p.T
+    cells = T * E
+    try:  # in one expression: a small call takes 6 us, the loops over names 2 of them
+        fits = (logits.dtype is _f32 and topk_idx.dtype is _i32 and counts.dtype is _i32 and losses.dtype is _f32
+                and (seq_offsets is None or seq_offsets.dtype is _i32)
+                and (dlogits is None or dlogits.dtype is _f32 and dlogits.numel() >= cells)
+                and logits.numel() >= cells and topk_idx.numel() >= T * p.k and counts.numel() >= n_seq * E
+                and losses.numel() >= 2)
+    except AttributeError:  # None or a plain address among them
+        fits = False
+    if not fits:
+        _refuse((("logits", logits, _f32), ("topk_idx", topk_idx, _i32), ("seq_offsets", seq_offsets, _i32),
+                 ("counts", counts, _i32), ("losses", losses, _f32), ("dlogits", dlogits, _f32)),
+                (("logits", logits, cells), ("topk_idx", topk_idx, T * p.k), ("counts", counts, n_seq * E),
+                 ("losses", losses, 2), ("dlogits", dlogits, cells)))
     _check(load().moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
                                    float(aux_coef), float(z_coef), _ptr(counts), _ptr(losses), _ptr(dlogits),
                                    _ptr(ws), _nbytes(ws), _stream(stream)))

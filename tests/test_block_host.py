@@ -185,3 +185,47 @@ def test_balance_counts_beyond_32_bits_are_refused():
     n = ctypes.c_size_t()
     assert status("moe_balance_workspace_size", ctypes.byref(prob(E=1024, k=2)), 1 << 21, ctypes.byref(n)) == 2
     assert status("moe_balance_workspace_size", ctypes.byref(prob(E=1024, k=2)), 1 << 20, ctypes.byref(n)) == 0
+
+
+# ------------------------------------------------- the binding: element types and sizes
+def balance_args(torch):
+    """A call of 64 tokens, 8 experts, 2 choices and 2 sequences, on the host: nothing
+    that is refused reads it."""
+    return dict(logits=torch.zeros(64, 8), topk_idx=torch.zeros(64, 2, dtype=torch.int32),
+                seq_offsets=torch.zeros(3, dtype=torch.int32), counts=torch.zeros(2, 8, dtype=torch.int32),
+                losses=torch.zeros(2), dlogits=torch.zeros(64, 8))
+
+
+@pytest.mark.parametrize("name,dtype", [
+    ("topk_idx", "int64"),       # what torch.topk returns
+    ("topk_idx", "float32"), ("seq_offsets", "float32"), ("seq_offsets", "int64"), ("logits", "bfloat16"),
+    ("logits", "float64"), ("dlogits", "bfloat16"), ("dlogits", "float16"), ("counts", "int64"), ("counts", "float32"),
+    ("losses", "float64"), ("losses", "int32")])
+def test_balance_binding_refuses_other_element_types(name, dtype):
+    torch = pytest.importorskip("torch")
+    a = balance_args(torch)
+    a[name] = a[name].to(getattr(torch, dtype))
+    with pytest.raises(TypeError, match=name):
+        moe.moe_balance_loss(prob(), **a, stream=0)
+
+
+@pytest.mark.parametrize("name,shape", [("logits", (63, 8)), ("topk_idx", (64, 1)), ("counts", (1, 8)), ("losses", (1,)),
+                                        ("dlogits", (64, 7))])
+def test_balance_binding_refuses_tensors_that_are_too_small(name, shape):
+    torch = pytest.importorskip("torch")
+    a = balance_args(torch)
+    a[name] = a[name].new_zeros(shape)
+    with pytest.raises(ValueError, match=name):
+        moe.moe_balance_loss(prob(), **a, stream=0)
+
+
+def test_balance_binding_passes_what_fits():
+    """Larger buffers, no gradient and plain addresses reach the library (which
+    refuses the missing workspace)."""
+    torch = pytest.importorskip("torch")
+    a = balance_args(torch)
+    for change in (dict(), dict(dlogits=None), dict(counts=torch.zeros(5, 8, dtype=torch.int32), losses=torch.zeros(7)),
+                   dict(logits=FAKE, topk_idx=FAKE, counts=FAKE, losses=FAKE, dlogits=FAKE)):
+        with pytest.raises(moe.MoeError) as err:
+            moe.moe_balance_loss(prob(), **dict(a, **change), stream=0)
+        assert err.value.status == moe.MOE_ERR_WORKSPACE
