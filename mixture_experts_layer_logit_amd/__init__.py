@@ -334,36 +334,38 @@ def moe_backward(p, dy, x, Wg, W1, W2, logits, info, saved, dx, dWg, dbg, dW1, d
 
 
 _scale_types, _src_types = {}, {}
-_f32 = _i32 = None
+_f32 = _i32 = _bf16 = _codes = None
+_INFO = tuple(f for f, _ in RouteInfo._fields_)
 
 
 def _fill_types():
     import torch
-    global _f32, _i32
-    _f32, _i32 = torch.float32, torch.int32
+    global _f32, _i32, _bf16, _codes
+    _f32, _i32, _bf16 = torch.float32, torch.int32, torch.bfloat16
+    _codes = (torch.uint8, torch.float8_e4m3fn, torch.int8)
     _scale_types.update({torch.float32: MOE_SCALE_F32, torch.uint8: MOE_SCALE_E8M0,
                          torch.float8_e8m0fnu: MOE_SCALE_E8M0})
     _src_types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
 
 
-def _refuse(types, sizes):
-    """TypeError for the first (name, tensor, type) whose tensor has another element
-    type, ValueError for the first (name, tensor, least) with fewer elements: the
-    kernels would read the bytes as something else, or go past their end."""
-    def tensor(t):
-        return t is not None and not isinstance(t, int)  # plain addresses pass
-
+def _refuse(types, sizes=()):
+    """TypeError for the first (name, tensor, type or types) whose tensor has another
+    element type, ValueError for the first (name, tensor, least) with fewer elements:
+    the kernels would read the bytes as something else, or go past their end.  None
+    and plain addresses pass."""
     for name, t, kind in types:
-        if tensor(t) and t.dtype is not kind:
-            raise TypeError(f"{name}: {kind}, not {t.dtype}")
+        if t is None or isinstance(t, int):
+            continue
+        if (t.dtype not in kind) if kind is _codes else (t.dtype is not kind):
+            raise TypeError(f"{name}: {' or '.join(map(str, kind[:2])) if kind is _codes else kind}, not {t.dtype}")
     for name, t, least in sizes:
-        if tensor(t) and t.numel() < least:
+        if t is not None and not isinstance(t, int) and t.numel() < least:
             raise ValueError(f"{name}: {t.numel()} elements, {least} are needed")
 
 
 def _scale_type(scales) -> int:
     """MOE_SCALE_* of a tensor of block scales, by its element type."""
-    if not _scale_types:
+    if _f32 is None:
         _fill_types()
     kind = _scale_types.get(scales.dtype)
     if kind is None:
@@ -380,14 +382,19 @@ def _e8m0(scales, name):
 def moe_quantize_fp8_block(src, codes, scales, block_rows=1, stream=None):
     """Rows of src (fp32 or bf16 tensor [rows, K]) to E4M3 codes (uint8 [rows, K])
     with a power-of-two scale per block of block_rows (1 or 128) x 128 values;
-    scales [ceil(rows / block_rows), K / 128] is uint8 / float8_e8m0fnu (E8M0) or fp32."""
+    scales [ceil(rows / block_rows), K / 128] is uint8 / float8_e8m0fnu (E8M0) or fp32.
+    Here and below codes may also be float8_e4m3fn; other types raise TypeError,
+    outputs with too few elements ValueError."""
     kind = _scale_type(scales)
     dt = _src_types.get(src.dtype)
     if dt is None:
         raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
-    K = src.shape[-1]
-    _check(load().moe_quantize_fp8_block(_ptr(src), dt, src.numel() // (K or 1), K, int(block_rows), _ptr(codes),
-                                         _ptr(scales), kind, _stream(stream)))
+    n, K = src.numel(), src.shape[-1]
+    rows = n // (K or 1)
+    least = (-(-rows // block_rows) if block_rows > 1 else rows) * (K // 128)
+    _refuse((("codes", codes, _codes),), (("codes", codes, n), ("scales", scales, least)))
+    _check(load().moe_quantize_fp8_block(_ptr(src), dt, rows, K, int(block_rows), _ptr(codes), _ptr(scales), kind,
+                                         _stream(stream)))
 
 
 def moe_fp8_block_workspace_size(p) -> int:
@@ -399,14 +406,19 @@ def moe_fp8_block_workspace_size(p) -> int:
 def moe_expert_up_fp8_block(p, aq, a_scale, src_token, offsets, W1q, w1s, hq, hs, ws=None, stream=None):
     """aq, a_scale: codes and E8M0 scales of x (rows gathered through src_token) or
     of the permuted rows (src_token None); w1s: E8M0 or fp32 scales; hq, hs: out."""
+    kind = _scale_type(w1s)
+    _refuse((("aq", aq, _codes), ("src_token", src_token, _i32), ("offsets", offsets, _i32), ("W1q", W1q, _codes),
+             ("hq", hq, _codes)))
     _check(load().moe_expert_up_fp8_block(ctypes.byref(p), _ptr(aq), _ptr(_e8m0(a_scale, "a_scale")),
-                                          _ptr(src_token), _ptr(offsets), _ptr(W1q), _ptr(w1s), _scale_type(w1s),
+                                          _ptr(src_token), _ptr(offsets), _ptr(W1q), _ptr(w1s), kind,
                                           _ptr(hq), _ptr(_e8m0(hs, "hs")), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_expert_down_fp8_block(p, hq, hs, offsets, W2q, w2s, y_perm, ws=None, stream=None):
+    kind = _scale_type(w2s)
+    _refuse((("hq", hq, _codes), ("offsets", offsets, _i32), ("W2q", W2q, _codes), ("y_perm", y_perm, _bf16)))
     _check(load().moe_expert_down_fp8_block(ctypes.byref(p), _ptr(hq), _ptr(_e8m0(hs, "hs")), _ptr(offsets),
-                                            _ptr(W2q), _ptr(w2s), _scale_type(w2s), _ptr(y_perm), _ptr(ws),
+                                            _ptr(W2q), _ptr(w2s), kind, _ptr(y_perm), _ptr(ws),
                                             _nbytes(ws), _stream(stream)))
 
 
@@ -415,6 +427,26 @@ def moe_forward_fp8_block(p, x, Wg, bg, W1q, w1s, W2q, w2s, y, logits=None, info
     kind = _scale_type(w1s)
     if _scale_type(w2s) != kind:
         raise TypeError("w1s and w2s must be scales of one type")
+    T, E = p.T, p.E
+    n = T * p.d
+    try:  # as in moe_balance_loss: the loops over names take 4 us
+        fits = (x.dtype is _bf16 and y.dtype is _bf16 and W1q.dtype in _codes and W2q.dtype in _codes
+                and (Wg is None or Wg.dtype is _bf16) and (bg is None or bg.dtype is _f32)
+                and (logits is None or logits.dtype is _f32 and logits.numel() >= T * E)
+                and x.numel() >= n and y.numel() >= n)
+    except AttributeError:
+        fits = False
+    if not fits:
+        _refuse((("x", x, _bf16), ("Wg", Wg, _bf16), ("bg", bg, _f32), ("W1q", W1q, _codes), ("W2q", W2q, _codes),
+                 ("y", y, _bf16), ("logits", logits, _f32)), (("x", x, n), ("y", y, n), ("logits", logits, T * E)))
+    if info:
+        least, choices = {"counts": E, "offsets": E + 1}, T * p.k
+        for f in _INFO:
+            t = info.get(f)
+            if t is not None and not isinstance(t, int):
+                of, n = _f32 if f == "topk_w" else _i32, least.get(f, choices)
+                if t.dtype is not of or t.numel() < n:
+                    _refuse(((f, t, of),), ((f, t, n),))
     ri = _route_info(info) if info else None
     _check(load().moe_forward_fp8_block(ctypes.byref(p), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1q), _ptr(w1s),
                                         _ptr(W2q), _ptr(w2s), kind, _ptr(y), _ptr(logits),

@@ -229,3 +229,101 @@ def test_balance_binding_passes_what_fits():
         with pytest.raises(moe.MoeError) as err:
             moe.moe_balance_loss(prob(), **dict(a, **change), stream=0)
         assert err.value.status == moe.MOE_ERR_WORKSPACE
+
+
+def fp8_block_calls(torch):
+    """Arguments of the right types and sizes for every block FP8 entry point, on the
+    host: nothing that is refused reads them."""
+    T, d, E, k, F = 64, 256, 8, 2, 384
+
+    def u8(*shape):
+        return torch.zeros(*shape, dtype=torch.uint8)
+
+    def i32(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    def bf(*shape):
+        return torch.zeros(*shape, dtype=torch.bfloat16)
+
+    w1, s1, w2, s2 = u8(E, 2 * F, d), u8(E, 2 * F // 128, d // 128), u8(E, d, F), u8(E, d // 128, F // 128)
+    return {
+        "moe_quantize_fp8_block": dict(src=bf(T, d), codes=u8(T, d), scales=u8(T, d // 128)),
+        "moe_expert_up_fp8_block": dict(p=prob(), aq=u8(T, d), a_scale=u8(T, d // 128), src_token=i32(T * k), offsets=i32(E + 1),
+                                        W1q=w1, w1s=s1, hq=u8(T * k, F), hs=u8(T * k, F // 128)),
+        "moe_expert_down_fp8_block": dict(p=prob(), hq=u8(T * k, F), hs=u8(T * k, F // 128), offsets=i32(E + 1), W2q=w2, w2s=s2,
+                                          y_perm=bf(T * k, d)),
+        "moe_forward_fp8_block": dict(p=prob(), x=bf(T, d), Wg=bf(E, d), bg=torch.zeros(E), W1q=w1, w1s=s1, W2q=w2, w2s=s2,
+                                      y=bf(T, d), logits=torch.zeros(T, E),
+                                      info=dict(topk_idx=i32(T, k), topk_w=torch.zeros(T, k), counts=i32(E), offsets=i32(E + 1),
+                                                slot=i32(T, k), src_token=i32(T * k)))}
+
+
+@pytest.mark.parametrize("fn,name,dtype", [
+    ("moe_quantize_fp8_block", "codes", "float32"), ("moe_quantize_fp8_block", "codes", "float8_e4m3fnuz"),
+    ("moe_expert_up_fp8_block", "aq", "bfloat16"), ("moe_expert_up_fp8_block", "aq", "float8_e5m2"),
+    ("moe_expert_up_fp8_block", "src_token", "int64"), ("moe_expert_up_fp8_block", "offsets", "int64"),
+    ("moe_expert_up_fp8_block", "W1q", "bfloat16"), ("moe_expert_up_fp8_block", "hq", "bfloat16"),
+    ("moe_expert_down_fp8_block", "hq", "bfloat16"), ("moe_expert_down_fp8_block", "offsets", "float32"),
+    ("moe_expert_down_fp8_block", "W2q", "float32"), ("moe_expert_down_fp8_block", "y_perm", "float32"),
+    ("moe_expert_down_fp8_block", "y_perm", "float16"),
+    ("moe_forward_fp8_block", "x", "float16"), ("moe_forward_fp8_block", "x", "float32"),
+    ("moe_forward_fp8_block", "Wg", "float32"), ("moe_forward_fp8_block", "bg", "bfloat16"),
+    ("moe_forward_fp8_block", "W1q", "bfloat16"), ("moe_forward_fp8_block", "W2q", "bfloat16"),
+    ("moe_forward_fp8_block", "y", "float16"), ("moe_forward_fp8_block", "logits", "bfloat16"),
+    ("moe_forward_fp8_block", "topk_idx", "int64"), ("moe_forward_fp8_block", "topk_w", "bfloat16"),
+    ("moe_forward_fp8_block", "src_token", "int64")])
+def test_block_bindings_refuse_other_element_types(fn, name, dtype):
+    torch = pytest.importorskip("torch")
+    a = fp8_block_calls(torch)[fn]
+    holder = a if name in a else a["info"]
+    holder[name] = torch.zeros(holder[name].shape).to(getattr(torch, dtype))
+    with pytest.raises(TypeError, match=name):
+        getattr(moe, fn)(**a, stream=0)
+
+
+@pytest.mark.parametrize("fn,name,shape", [
+    ("moe_quantize_fp8_block", "codes", (63, 256)), ("moe_quantize_fp8_block", "scales", (64, 1)),
+    ("moe_forward_fp8_block", "x", (63, 256)), ("moe_forward_fp8_block", "y", (63, 256)),
+    ("moe_forward_fp8_block", "logits", (64, 7)), ("moe_forward_fp8_block", "topk_idx", (64, 1)),
+    ("moe_forward_fp8_block", "offsets", (8,))])
+def test_block_bindings_refuse_tensors_that_are_too_small(fn, name, shape):
+    torch = pytest.importorskip("torch")
+    a = fp8_block_calls(torch)[fn]
+    holder = a if name in a else a["info"]
+    holder[name] = holder[name].new_zeros(shape)
+    with pytest.raises(ValueError, match=name):
+        getattr(moe, fn)(**a, stream=0)
+
+
+@pytest.mark.parametrize("block_rows,scales", [(1, 7 * 2), (128, 2)])
+def test_quantiser_sizes_count_the_blocks(block_rows, scales):
+    """7 rows of 256 values: enough scales pass on to the library (which refuses
+    the odd address), one fewer does not."""
+    torch = pytest.importorskip("torch")
+    src, codes = torch.zeros(8, 256)[1:].bfloat16(), torch.zeros(7 * 256 + 8, dtype=torch.uint8)[8:]
+    with pytest.raises(moe.MoeError):
+        moe.moe_quantize_fp8_block(src, codes, torch.zeros(scales, dtype=torch.uint8), block_rows=block_rows, stream=0)
+    with pytest.raises(ValueError, match="scales"):
+        moe.moe_quantize_fp8_block(src, codes, torch.zeros(scales - 1, dtype=torch.uint8), block_rows=block_rows, stream=0)
+
+
+def test_block_bindings_pass_what_fits():
+    """Codes as float8_e4m3fn, scales as float8_e8m0fnu, larger buffers and plain
+    addresses reach the library, which refuses the workspace."""
+    torch = pytest.importorskip("torch")
+    a = fp8_block_calls(torch)
+    small = torch.zeros(16, dtype=torch.uint8)
+    for bad in (None, FAKE + 8):
+        with pytest.raises(moe.MoeError, match="codes"):
+            moe.moe_quantize_fp8_block(**dict(a["moe_quantize_fp8_block"], codes=bad), stream=0)
+    for fn in ("moe_expert_up_fp8_block", "moe_expert_down_fp8_block", "moe_forward_fp8_block"):
+        plain, typed = dict(a[fn]), dict(a[fn])
+        for n, t in a[fn].items():
+            if torch.is_tensor(t) and t.dtype is torch.uint8:
+                typed[n] = t.view(torch.float8_e8m0fnu if n in ("a_scale", "hs", "w1s", "w2s") else torch.float8_e4m3fn)
+            elif torch.is_tensor(t):
+                plain[n] = FAKE
+        for call in (a[fn], plain, typed, dict(a[fn], **({"y": torch.zeros(65, 256).bfloat16()} if "y" in a[fn] else {}))):
+            with pytest.raises(moe.MoeError) as err:
+                getattr(moe, fn)(**call, ws=small, stream=0)
+            assert err.value.status == moe.MOE_ERR_WORKSPACE
