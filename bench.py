@@ -54,16 +54,22 @@ METRIC = "MoE-layer fwd tokens/sec at Mixtral shape; grouped-GEMM % of bf16 MFMA
 PEAK_TFLOPS = {"bf16": 2500.0, "f32": 157.3, "fp8": 5000.0}   # MI355X dense MFMA peaks
 HBM_GBPS = 8000.0
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
-GEMM_SRC = os.path.join(ROOT, "mixture_experts_layer_logit_amd", "csrc", "grouped_gemm.hip")
+CSRC = os.path.join(ROOT, "mixture_experts_layer_logit_amd", "csrc")
+# what the grouped GEMM's kernels are compiled from: the stored counters hold for these texts only
+GEMM_SRC = ("grouped_gemm.hip", "gemm_common.h", "common.h")
 
 
 def log(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
-def source_hash(path: str) -> str:
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+def source_hash(names=GEMM_SRC, folder=None) -> str:
+    h = hashlib.sha256()
+    for name in names:
+        with open(os.path.join(folder or CSRC, name), "rb") as f:
+            text = f.read()
+        h.update(f"{name} {len(text)}\n".encode() + text)
+    return h.hexdigest()[:16]
 
 
 def stored_traffic(config: str):
@@ -75,7 +81,7 @@ def stored_traffic(config: str):
     except (OSError, ValueError):
         return None
     entry = t.get(config)
-    if not entry or entry.get("kernel_source_sha256_16") != source_hash(GEMM_SRC):
+    if not entry or entry.get("kernel_source_sha256_16") != source_hash():
         return None
     return entry.get("bytes_per_launch")
 
