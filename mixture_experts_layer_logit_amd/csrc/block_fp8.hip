@@ -788,12 +788,13 @@ using namespace moe;
 //    2048   128  1024   45.9 / 69.8    50.5 / 52.1
 // so (narrow_pays) up to a tile a CU; up to two where K is below 2048, where the
 // choice would be the 256-row tile, or with fp32 scales from 64 rows on; and any
-// number below 192 rows for K below 2048 with fp32 scales or few rows.  From 192 rows
-// on with fp32 scales the 128-row tile is the better one above two a CU: 64 x 128
-// takes 1.1 to 1.4 times as long on 1024 to 4096 tiles of 200, 300 and 512 rows (K 512
-// to 1920), 0.87 to 0.91 where rows just past a multiple of 128 leave the 128-row
-// tiles a second, nearly empty round (8 or 16 experts of about 256 rows, the table's
-// fp32 line; 64 of them 1.03 to 1.17).
+// number below 192 rows for K below 2048 with fp32 scales or few rows.  With fp32
+// scales, 192 rows or more and more than two tiles a CU the 128-row tile is the
+// better one at most sizes (K 512 to 1920, time of 64 x 128 over its time): 1.1 to 1.4
+// for 1024 to 4096 tiles of 256, 512 or 2048 rows each, 0.97 to 1.3 for ragged
+// segments of about 200, 300 and 512; but 0.87 to 0.94 where 8 or 16 experts of about
+// 256 rows leave it a second, nearly empty round (the table's fp32 line), and 0.73 to
+// 0.91 where 640 columns end inside its last 256.
 typedef BlockShape<256, 2, 4, 2, 8> LargeShape;
 typedef BlockShape<128, 2, 4, 3, 8> Shape128;
 typedef BlockShape<96, 1, 4, 3, 4> MediumShape;
