@@ -391,8 +391,13 @@ def moe_quantize_fp8_block(src, codes, scales, block_rows=1, stream=None):
         raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
     n, K = src.numel(), src.shape[-1]
     rows = n // (K or 1)
-    least = (-(-rows // block_rows) if block_rows > 1 else rows) * (K // 128)
-    _refuse((("codes", codes, _codes),), (("codes", codes, n), ("scales", scales, least)))
+    least = (rows if block_rows <= 1 else -(-rows // block_rows)) * (K // 128)
+    try:  # as in moe_balance_loss
+        fits = codes.dtype in _codes and codes.numel() >= n and scales.numel() >= least
+    except AttributeError:
+        fits = False
+    if not fits:
+        _refuse((("codes", codes, _codes),), (("codes", codes, n), ("scales", scales, least)))
     _check(load().moe_quantize_fp8_block(_ptr(src), dt, rows, K, int(block_rows), _ptr(codes), _ptr(scales), kind,
                                          _stream(stream)))
 
