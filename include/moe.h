@@ -398,7 +398,8 @@ moe_status moe_forward_fp8(const moe_problem* p, const void* x, const void* Wg, 
  *     W2q [E][d][F] codes,  w2s [E][d/128][F/128]
  *     MOE_SCALE_E8M0: bytes; gfx950's matrix cores apply both scales of a block
  *     themselves.  MOE_SCALE_F32: fp32 numbers, any finite value (a
- *     checkpoint's own scales); each block's product is scaled in fp32.
+ *     checkpoint's own scales); each block's product, times its activation scale
+ *     an fp32 number, is scaled in fp32.
  * An E8M0 byte of 255 is NaN.  Requirements beyond the common limits:
  * problem->dtype == MOE_BF16, d and F multiples of 128.  Codes must be 16-byte
  * aligned, fp32 scales 4-byte, E8M0 scales need no alignment.  A NaN

@@ -174,3 +174,39 @@ def test_layer_on_wide_tiles(shape, f32):
 def test_layer_of_many_choices(shape, f32):
     """Four to eight choices a token, some of them dropped."""
     base.test_layer(shape, f32)
+
+
+@pytest.mark.parametrize("shape", [(9, 384, 2, 1, 256, "relu", "even"), (300, 384, 2, 1, 256, "swiglu", "even")],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_the_outermost_e8m0_scales(shape):
+    """Bytes 0 and 254 on either side, whose products stay in range."""
+    c = base.Case(*shape, False)
+    c.xs[:, 0], c.xs[:, 1], c.xs[:, 2] = 0, 254, 100
+    c.x = ref.widen_rows(c.xq, c.xs.astype(np.int64) - 127)
+    c.s1[:, :, 0], c.s1[:, :, 1], c.s1[:, :, 2] = 250, 0, 140
+    c.hs[:, 0], c.hs[:, 1] = 0, 254
+    c.h = ref.widen_rows(c.hq, c.hs.astype(np.int64) - 127)
+    c.s2[:, :, 0], c.s2[:, :, 1] = 254, 0
+    for e in range(c.E):
+        c.w1[e] = ref.widen_matrix(c.W1[e], np.exp2(c.s1[e].astype(np.float64) - 127))
+        c.w2[e] = ref.widen_matrix(c.W2[e], np.exp2(c.s2[e].astype(np.float64) - 127))
+    c.check_up(*c.up())
+    c.check_down(c.down())
+
+
+@pytest.mark.parametrize("shape", [(9, 640, 2, 1, 640, "relu", "even"), (300, 640, 2, 1, 640, "swiglu", "even")],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_fp32_scales_of_every_kind(shape):
+    """Negative, zero, subnormal, tiny and large weight scales."""
+    c = base.Case(*shape, True)
+    for s in (c.s1, c.s2):
+        s[:, :, 0] *= -1
+        s[:, :, 1] = 0
+        s[:, :, 2] = 1e-40
+        s[:, ::2, 3] *= 2.0 ** 20
+        s[:, 1::2, 3] *= 2.0 ** -30
+    for e in range(c.E):
+        c.w1[e] = ref.widen_matrix(c.W1[e], c.s1[e])
+        c.w2[e] = ref.widen_matrix(c.W2[e], c.s2[e])
+    c.check_up(*c.up())
+    c.check_down(c.down())
