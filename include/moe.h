@@ -26,11 +26,17 @@
  *   moe_quantize_fp8_block, moe_expert_up_fp8_block, moe_expert_down_fp8_block,
  *   moe_forward_fp8_block
  *                    the layer with FP8 experts scaled by blocks of 128
+ *   moe_quantize_mxfp4, moe_dequantize_mxfp4, moe_expert_up_mxfp4,
+ *   moe_expert_down_mxfp4, moe_forward_mxfp4
+ *                    the layer with 4-bit (MXFP4) expert weights and activations
  *   moe_balance_loss per-sequence balance and Z losses of a padded batch, expert
  *                    counts, and the gradient of the logits
  *   moe_forward_train, moe_backward
  *                    training: the forward keeping its intermediates, and the
  *                    gradients of every input and weight
+ *   moe_orthogonalize
+ *                    momentum and Newton-Schulz orthogonalisation of weight
+ *                    gradients: the optimiser's update of the experts
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -454,6 +460,66 @@ moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void
                                  int32_t w_scale, void* y, float* logits, const moe_route_info* info, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------ MXFP4 experts
+ * The layer with 4-bit weights and activations: half the bytes of FP8 experts for
+ * a decoding batch, whose time is the weights', and twice their matrix rate for a
+ * prompt.  Every row of a weight matrix, of x and of h is held in blocks of 32
+ * consecutive values: OCP E2M1 codes (sign, 2 exponent bits, 1 mantissa bit: 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte with the even value in the low four
+ * bits, and one E8M0 byte b that stands for the scale 2^(b-127).
+ *     xq [T][d/2] codes, xs [T][d/32];  hq [T*k][F/2] codes, hs [T*k][F/32]
+ *     W1q [E][n1][d/2] codes, w1s [E][n1][d/32]  (gate rows first for SwiGLU)
+ *     W2q [E][d][F/2] codes,  w2s [E][d][F/32]
+ * gfx950's matrix cores apply both scales of a block themselves; sums are fp32.
+ * Requirements beyond the common limits: problem->dtype == MOE_BF16, d and F
+ * multiples of 128.  Codes must be 16-byte aligned, scales 4-byte aligned.  A scale
+ * byte of 255 makes its block NaN, and so the rows its products end up in. */
+
+/* Quantise rows rows of K values (src_dtype MOE_F32 or MOE_BF16; K a multiple of
+ * 32).  Every block gets the smallest power of two s with max|block| <= 6 s, at
+ * least 2^-127 (s = 1 for an all-zero block), and the E2M1 codes nearest to v / s
+ * (ties to the even code); no value is clipped.  A block with a NaN or an infinity
+ * gets the scale byte 255.  codes [rows][K/2], scales [rows][K/32] (any alignment).
+ * The weights of E experts are E*n1 (or E*d) rows.  No workspace. */
+moe_status moe_quantize_mxfp4(const void* src, int32_t src_dtype, int64_t rows, int32_t K, uint8_t* codes,
+                              uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for, in fp32 or bf16 (dst_dtype; dst
+ * [rows][K]).  They are exact in both types, but for scales from 2^126 on, whose
+ * largest codes are infinite.  Blocks of scale byte 255 are NaN. */
+moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K, void* dst,
+                                int32_t dst_dtype, void* stream);
+
+/* Bytes of workspace that suffice for every entry point below of this
+ * problem.  Host only. */
+moe_status moe_mxfp4_workspace_size(const moe_problem* p, size_t* bytes);
+
+/* First expert layer: u = W1[e] a_r on such codes for r in expert e's segment, h =
+ * max(u, 0) or silu(u_f) u_{F+f} in fp32, quantised as moe_quantize_mxfp4 does: hq
+ * [T*k][F/2], hs [T*k][F/32].  aq and as are those of x when src_token is given
+ * (rows gathered on the fly; T*d/2 below 0xF0000000 bytes, else
+ * MOE_ERR_UNSUPPORTED), of the permuted rows when it is NULL.  Rows from
+ * offsets[E] on are left as they were.  offsets as in moe_expert_up.  ws
+ * (nullable; if given, ws_bytes >= moe_mxfp4_workspace_size) lets the last round of
+ * output tiles be split along K, its parts added in a fixed order. */
+moe_status moe_expert_up_mxfp4(const moe_problem* p, const uint8_t* aq, const uint8_t* as, const int32_t* src_token,
+                               const int32_t* offsets, const uint8_t* W1q, const uint8_t* w1s, uint8_t* hq,
+                               uint8_t* hs, void* ws, size_t ws_bytes, void* stream);
+
+/* Second expert layer: y_perm[r] = W2[e] h[r] from such codes, bf16 out.  Rows
+ * from offsets[E] on are left as they were.  ws as above. */
+moe_status moe_expert_down_mxfp4(const moe_problem* p, const uint8_t* hq, const uint8_t* hs, const int32_t* offsets,
+                                 const uint8_t* W2q, const uint8_t* w2s, void* y_perm, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* The whole layer: route and permute as moe_forward, quantise x, both expert
+ * layers on codes, combine.  The expert outputs stay in fp32 up to the combine: y
+ * is rounded to bf16 once.  Other arguments as moe_forward.  Needs ws_bytes >=
+ * moe_mxfp4_workspace_size; T*d/2 >= 0xF0000000 returns MOE_ERR_UNSUPPORTED. */
+moe_status moe_forward_mxfp4(const moe_problem* p, const void* x, const void* Wg, const float* bg, const uint8_t* W1q,
+                             const uint8_t* w1s, const uint8_t* W2q, const uint8_t* w2s, void* y, float* logits,
+                             const moe_route_info* info, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------ balance loss of sequences
  * moe_router_stats' auxiliary and Z losses (Megatron-Core page,
  * "MoE负载均衡的挑战与应对" and "关键特性"; Skywork news, 技术创新 2) with the
@@ -484,6 +550,30 @@ moe_status moe_balance_workspace_size(const moe_problem* p, int32_t n_seq, size_
 moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
                             const int32_t* seq_offsets, int32_t n_seq, float aux_coef, float z_coef, int32_t* counts,
                             float* losses, float* dlogits, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------ orthogonalised updates
+ * What the Muon optimiser (K. Jordan et al., "Muon: an optimizer for hidden layers
+ * in neural networks", 2024) makes of a weight gradient, for a batch of count
+ * matrices [rows][cols] at once: dW1 of E ReLU experts is E matrices [F][d], of E
+ * SwiGLU experts 2E of them, dW2 E matrices [d][F], dWg one [E][d].
+ *   momentum given:  M <- beta M + G (fp32, written);  U = G + beta M where
+ *                    nesterov, else M
+ *   momentum NULL:   U = G
+ *   X = U / |U|_F (zero where U is), then steps times, on the orientation of X with
+ *   the fewer rows:  A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A^2) X
+ *   out [count][rows][cols] = X, rounded to bf16 once
+ * G is fp32 (as moe_backward writes it) or bf16 (grad_dtype).  |U|_F is summed in
+ * fp64, in a fixed order.  The products run on fp16 operands with fp32 sums,
+ * scaled so that no range is lost: out is within about 1.5e-3 of the 64-bit result
+ * in the norm before its rounding.  The same bits on every run.  A matrix whose U
+ * holds a NaN or an infinity becomes NaN as a whole and leaves the others alone.
+ * 1 <= rows, cols <= 65536 (any size, no alignment beyond an element's), rows *
+ * cols < 2^30, 0 <= count <= 32768, 1 <= steps <= 64 (5 is usual).  Needs ws_bytes
+ * >= moe_orthogonalize_workspace_size (16-byte aligned). */
+moe_status moe_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t cols, size_t* bytes);
+moe_status moe_orthogonalize(const void* grad, int32_t grad_dtype, float* momentum, float beta, int32_t nesterov,
+                             int32_t count, int32_t rows, int32_t cols, int32_t steps, void* out, void* ws,
+                             size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,9 @@ moe_expert_up_fp8, moe_expert_down_fp8, moe_forward_fp8, moe_forward_train,
 moe_backward_workspace_size, moe_backward, moe_forward_noalloc,
 moe_quantize_fp8_block, moe_fp8_block_workspace_size, moe_expert_up_fp8_block,
 moe_expert_down_fp8_block, moe_forward_fp8_block, moe_balance_workspace_size,
-moe_balance_loss.
+moe_balance_loss, moe_quantize_mxfp4, moe_dequantize_mxfp4,
+moe_mxfp4_workspace_size, moe_expert_up_mxfp4, moe_expert_down_mxfp4,
+moe_forward_mxfp4, moe_orthogonalize_workspace_size, moe_orthogonalize.
 """
 from __future__ import annotations
 
@@ -36,7 +38,9 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_capacity", "moe_workspace
            "moe_forward_fp8", "moe_forward_train", "moe_backward_workspace_size", "moe_backward",
            "moe_forward_noalloc", "moe_quantize_fp8_block", "moe_fp8_block_workspace_size",
            "moe_expert_up_fp8_block", "moe_expert_down_fp8_block", "moe_forward_fp8_block",
-           "moe_balance_workspace_size", "moe_balance_loss")
+           "moe_balance_workspace_size", "moe_balance_loss", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+           "moe_mxfp4_workspace_size", "moe_expert_up_mxfp4", "moe_expert_down_mxfp4", "moe_forward_mxfp4",
+           "moe_orthogonalize_workspace_size", "moe_orthogonalize")
 
 
 class MoeError(RuntimeError):
@@ -115,6 +119,14 @@ def load() -> ctypes.CDLL:
     lib.moe_forward_fp8_block.argtypes = [PP, P, P, P, P, P, P, P, i32, P, P, ctypes.POINTER(RouteInfo), P, size, P]
     lib.moe_balance_workspace_size.argtypes = [PP, i32, ctypes.POINTER(size)]
     lib.moe_balance_loss.argtypes = [PP, P, P, P, i32, ctypes.c_float, ctypes.c_float, P, P, P, P, size, P]
+    lib.moe_quantize_mxfp4.argtypes = [P, i32, ctypes.c_int64, i32, P, P, P]
+    lib.moe_dequantize_mxfp4.argtypes = [P, P, ctypes.c_int64, i32, P, i32, P]
+    lib.moe_mxfp4_workspace_size.argtypes = [PP, ctypes.POINTER(size)]
+    lib.moe_expert_up_mxfp4.argtypes = [PP, P, P, P, P, P, P, P, P, P, size, P]
+    lib.moe_expert_down_mxfp4.argtypes = [PP, P, P, P, P, P, P, P, size, P]
+    lib.moe_forward_mxfp4.argtypes = [PP, P, P, P, P, P, P, P, P, P, ctypes.POINTER(RouteInfo), P, size, P]
+    lib.moe_orthogonalize_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(size)]
+    lib.moe_orthogonalize.argtypes = [P, i32, P, ctypes.c_float, i32, i32, i32, i32, i32, P, P, size, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = st
     _lib = lib
@@ -491,3 +503,167 @@ def moe_balance_loss(p, logits, topk_idx, seq_offsets, counts, losses, dlogits, 
     _check(load().moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), n_seq,
                                    float(aux_coef), float(z_coef), _ptr(counts), _ptr(losses), _ptr(dlogits),
                                    _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+_packed = ()
+
+
+def _fill_packed():
+    import torch
+    global _packed
+    if _f32 is None:
+        _fill_types()
+    _packed = (torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8))
+
+
+def _mx_check(codes=(), scales=(), others=()):
+    """TypeError or ValueError for the first (name, tensor, least bytes or elements)
+    that is no MXFP4 codes, no E8M0 scales or, of others (name, tensor, type, least),
+    another type, or that has too few elements: the kernels would read the bytes as
+    something else, or go past their end.  None and plain addresses pass."""
+    if not _packed:
+        _fill_packed()
+    for name, t, least in codes:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype not in _packed:
+            raise TypeError(f"{name}: MXFP4 codes are uint8 (two to a byte), not {t.dtype}")
+        if t.numel() < least:
+            raise ValueError(f"{name}: {t.numel()} bytes, {least} are needed")
+    for name, t, least in scales:
+        if t is None or isinstance(t, int):
+            continue
+        if _scale_types.get(t.dtype) != MOE_SCALE_E8M0:
+            raise TypeError(f"{name}: scales are E8M0 (uint8 or float8_e8m0fnu), not {t.dtype}")
+        if t.numel() < least:
+            raise ValueError(f"{name}: {t.numel()} elements, {least} are needed")
+    if others:
+        _refuse(((n, t, of) for n, t, of, _ in others), ((n, t, least) for n, t, _, least in others))
+
+
+def _on_gpu(stream, **tensors):
+    """ValueError for a tensor that is not on the GPU the call runs on: the current
+    one, or any single one where a stream is given.  None and plain addresses pass."""
+    at = None
+    for name, t in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        here = t.get_device()
+        if here < 0:
+            raise ValueError(f"{name} is not on a GPU")
+        if at is None:
+            if stream is None:
+                import torch
+                at = torch.cuda.current_device()
+            else:
+                at = here
+        if here != at:
+            raise ValueError(f"{name} is on GPU {here}, not on GPU {at}")
+
+
+def moe_quantize_mxfp4(src, codes, scales, stream=None):
+    """Rows of src (fp32 or bf16 tensor [rows, K]) to MXFP4: E2M1 codes (uint8 [rows,
+    K / 2], two to a byte) and an E8M0 scale per 32 values (uint8 or float8_e8m0fnu
+    [rows, K / 32])."""
+    if not _packed:
+        _fill_packed()
+    dt = _src_types.get(src.dtype)
+    if dt is None:
+        raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
+    n, K = src.numel(), src.shape[-1]
+    if not (codes.dtype in _packed and _scale_types.get(scales.dtype) == MOE_SCALE_E8M0 and codes.numel() >= n // 2
+            and scales.numel() >= n // 32):
+        _mx_check((("codes", codes, n // 2),), (("scales", scales, n // 32),))
+    _on_gpu(stream, src=src, codes=codes, scales=scales)
+    _check(load().moe_quantize_mxfp4(_ptr(src), dt, n // (K or 1), K, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_dequantize_mxfp4(codes, scales, dst, stream=None):
+    """The values of MXFP4 codes and scales, into dst (fp32 or bf16 [rows, K])."""
+    if not _packed:
+        _fill_packed()
+    dt = _src_types.get(dst.dtype)
+    if dt is None:
+        raise TypeError(f"dst is float32 or bfloat16, not {dst.dtype}")
+    n, K = dst.numel(), dst.shape[-1]
+    if not (codes.dtype in _packed and _scale_types.get(scales.dtype) == MOE_SCALE_E8M0 and codes.numel() >= n // 2
+            and scales.numel() >= n // 32):
+        _mx_check((("codes", codes, n // 2),), (("scales", scales, n // 32),))
+    _on_gpu(stream, codes=codes, scales=scales, dst=dst)
+    _check(load().moe_dequantize_mxfp4(_ptr(codes), _ptr(scales), n // (K or 1), K, _ptr(dst), dt, _stream(stream)))
+
+
+def moe_mxfp4_workspace_size(p) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_mxfp4_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def moe_expert_up_mxfp4(p, aq, a_scale, src_token, offsets, W1q, w1s, hq, hs, ws=None, stream=None):
+    """aq, a_scale: codes and scales of x (rows gathered through src_token) or of the
+    permuted rows (src_token None); hq, hs: out."""
+    T, d, E, F, rows = p.T, p.d, p.E, p.F, p.T * p.k
+    n1, a = 2 * F if p.act == MOE_ACT_SWIGLU else F, rows if src_token is None else T
+    _mx_check((("aq", aq, a * d // 2), ("W1q", W1q, E * n1 * d // 2), ("hq", hq, rows * F // 2)),
+              (("a_scale", a_scale, a * d // 32), ("w1s", w1s, E * n1 * d // 32), ("hs", hs, rows * F // 32)),
+              (("src_token", src_token, _i32, rows), ("offsets", offsets, _i32, E + 1)))
+    _on_gpu(stream, aq=aq, a_scale=a_scale, src_token=src_token, offsets=offsets, W1q=W1q, w1s=w1s, hq=hq, hs=hs, ws=ws)
+    _check(load().moe_expert_up_mxfp4(ctypes.byref(p), _ptr(aq), _ptr(a_scale), _ptr(src_token), _ptr(offsets),
+                                      _ptr(W1q), _ptr(w1s), _ptr(hq), _ptr(hs), _ptr(ws), _nbytes(ws),
+                                      _stream(stream)))
+
+
+def moe_expert_down_mxfp4(p, hq, hs, offsets, W2q, w2s, y_perm, ws=None, stream=None):
+    d, E, F, rows = p.d, p.E, p.F, p.T * p.k
+    _mx_check((("hq", hq, rows * F // 2), ("W2q", W2q, E * d * F // 2)),
+              (("hs", hs, rows * F // 32), ("w2s", w2s, E * d * F // 32)),
+              (("offsets", offsets, _i32, E + 1), ("y_perm", y_perm, _bf16, rows * d)))
+    _on_gpu(stream, hq=hq, hs=hs, offsets=offsets, W2q=W2q, w2s=w2s, y_perm=y_perm, ws=ws)
+    _check(load().moe_expert_down_mxfp4(ctypes.byref(p), _ptr(hq), _ptr(hs), _ptr(offsets), _ptr(W2q), _ptr(w2s),
+                                        _ptr(y_perm), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_forward_mxfp4(p, x, Wg, bg, W1q, w1s, W2q, w2s, y, logits=None, info=None, ws=None, stream=None):
+    """The layer with MXFP4 experts."""
+    T, d, E, F = p.T, p.d, p.E, p.F
+    n1 = 2 * F if p.act == MOE_ACT_SWIGLU else F
+    _mx_check((("W1q", W1q, E * n1 * d // 2), ("W2q", W2q, E * d * F // 2)),
+              (("w1s", w1s, E * n1 * d // 32), ("w2s", w2s, E * d * F // 32)),
+              (("x", x, _bf16, T * d), ("Wg", Wg, _bf16, E * d), ("bg", bg, _f32, E), ("y", y, _bf16, T * d),
+               ("logits", logits, _f32, T * E)))
+    if info:
+        least, choices = {"counts": E, "offsets": E + 1}, T * p.k
+        _mx_check(others=[(f, info.get(f), _f32 if f == "topk_w" else _i32, least.get(f, choices)) for f in _INFO])
+    _on_gpu(stream, x=x, Wg=Wg, bg=bg, W1q=W1q, w1s=w1s, W2q=W2q, w2s=w2s, y=y, logits=logits, ws=ws,
+            **{f: info.get(f) for f in _INFO} if info else {})
+    ri = _route_info(info) if info else None
+    _check(load().moe_forward_mxfp4(ctypes.byref(p), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1q), _ptr(w1s), _ptr(W2q),
+                                    _ptr(w2s), _ptr(y), _ptr(logits), ctypes.byref(ri) if ri is not None else None,
+                                    _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_orthogonalize_workspace_size(count, rows, cols) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_orthogonalize_workspace_size(int(count), int(rows), int(cols), ctypes.byref(n)))
+    return n.value
+
+
+def moe_orthogonalize(grad, out, momentum=None, beta=0.95, nesterov=True, steps=5, ws=None, stream=None):
+    """The orthogonalised update of each matrix of grad (fp32 or bf16, [count, rows,
+    cols] or [rows, cols]) into out (bf16).  momentum (fp32, updated): M <- beta M + G,
+    of which the update is G + beta M (nesterov) or M; None: it is G, beta and
+    nesterov do not count."""
+    if _f32 is None:
+        _fill_types()
+    dt = _src_types.get(grad.dtype)
+    if dt is None:
+        raise TypeError(f"grad is float32 or bfloat16, not {grad.dtype}")
+    if grad.dim() not in (2, 3):
+        raise ValueError(f"grad is [count, rows, cols] or [rows, cols], not {tuple(grad.shape)}")
+    rows, cols = grad.shape[-2:]
+    count, n = (grad.shape[0] if grad.dim() == 3 else 1), grad.numel()
+    _refuse((("out", out, _bf16), ("momentum", momentum, _f32)), (("out", out, n), ("momentum", momentum, n)))
+    _on_gpu(stream, grad=grad, out=out, momentum=momentum, ws=ws)
+    _check(load().moe_orthogonalize(_ptr(grad), dt, _ptr(momentum), float(beta),
+                                    int(bool(nesterov) and momentum is not None), count, rows, cols, int(steps),
+                                    _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)))

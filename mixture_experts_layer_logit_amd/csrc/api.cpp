@@ -68,6 +68,18 @@ hipError_t moe_launch_block_gemm(int epi, int wf32, const uint8_t* A, const uint
                                  int mean_rows, int ncu, float* partial, hipStream_t stream);
 hipError_t moe_launch_combine_rows(const float* rows, const int32_t* slot, const float* topk_w, int T, int d, int k,
                                    int max_rows, void* y, hipStream_t stream);
+hipError_t moe_launch_mxfp4_quantize(int dtype, const void* src, long long blocks, uint8_t* codes, uint8_t* scales,
+                                     hipStream_t stream);
+hipError_t moe_launch_mxfp4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, long long blocks,
+                                       void* dst, hipStream_t stream);
+size_t moe_mxfp4_gemm_partial_bytes(int mean_rows);
+hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uint8_t* As, const int32_t* gather, int gather_rows,
+                                 const uint8_t* W, const uint8_t* Ws, uint8_t* Hq, uint8_t* Hs, void* Y,
+                                 const int32_t* offsets, int E, int K, int Nw, int Nout, int F, int max_rows,
+                                 int mean_rows, int ncu, float* partial, hipStream_t stream);
+size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols);
+hipError_t moe_launch_orthogonalize(int dtype, const void* grad, float* momentum, float beta, int nesterov, int count,
+                                    int rows, int cols, int steps, void* out, void* ws, int ncu, hipStream_t stream);
 size_t moe_balance_scratch_bytes(void);
 hipError_t moe_launch_balance(const float* logits, const int32_t* topk_idx, const int32_t* offsets, int S, int T,
                               int E, int k, int normalize, float lambda, float aux_coef, float z_coef,
@@ -85,6 +97,8 @@ constexpr int kMaxK = 8;
 constexpr int kMaxT = 1 << 24;
 constexpr int kMaxDim = 65536;
 constexpr int kMaxSeq = 1 << 20;  // sequences of a balance loss
+constexpr int kMaxSteps = 64;         // Newton-Schulz steps
+constexpr int kMaxMatrices = 32768;  // of one orthogonalising call
 constexpr size_t kAlign = 256;
 // The fused row gather of the up projection addresses x with 32-bit byte
 // offsets, and offsets from 0xF0000000 up are its out-of-range marker.
@@ -399,6 +413,11 @@ bool gather_ok_fp8(const moe_problem* p)
     return (unsigned long long)p->T * p->d < kGatherBytes;
 }
 
+bool gather_ok_mxfp4(const moe_problem* p)
+{
+    return (unsigned long long)p->T * (p->d / 2) < kGatherBytes;
+}
+
 // The bf16 layout, then the codes and scales of x and h.
 struct LayoutFp8 {
     Layout base;
@@ -536,6 +555,109 @@ moe_status do_down_fp8_block(const moe_problem* p, const uint8_t* hq, const uint
                                             nullptr, y_perm, offsets, p->E, p->F, p->d, p->d, p->F, p->T * p->k,
                                             mean_rows_of(p), cu_count(), partial, s),
                       "block FP8 expert down launch");
+}
+
+// ---- MXFP4 experts
+moe_status check_mxfp4(const moe_problem* p)
+{
+    CHECK(check_problem(p));
+    if (p->dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "the MXFP4 path takes bf16 activations (dtype MOE_BF16)");
+    if (p->d % 128 || p->F % 128)
+        return fail(MOE_ERR_UNSUPPORTED, "the MXFP4 path needs d and F multiples of 128 (d=%d, F=%d)", p->d, p->F);
+    return MOE_OK;
+}
+
+struct LayoutMxfp4 {
+    size_t topk_idx, topk_w, counts, offsets, slot, src_token, chunk_cnt, logits, partial, xq, xs, hq, hs, y_perm,
+        total;
+};
+
+LayoutMxfp4 layout_mxfp4_of(const moe_problem* p)
+{
+    LayoutMxfp4 L;
+    const size_t T = (size_t)p->T, k = (size_t)p->k, E = (size_t)p->E, d = (size_t)p->d, F = (size_t)p->F;
+    const size_t nchunks = (T + kChunk - 1) / kChunk;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round_up(bytes);
+        return at;
+    };
+    L.topk_idx = take(T * k * 4);
+    L.topk_w = take(T * k * 4);
+    L.counts = take(E * 4);
+    L.offsets = take((E + 1) * 4);
+    L.slot = take(T * k * 4);
+    L.src_token = take(T * k * 4);
+    L.chunk_cnt = take(std::max<size_t>(nchunks, 1) * E * 4);
+    L.logits = take(T * E * 4);
+    L.partial = take(moe_mxfp4_gemm_partial_bytes(mean_rows_of(p)));
+    L.xq = take(T * (d / 2));
+    L.xs = take(T * (d / 32));
+    L.hq = take(T * k * (F / 2));
+    L.hs = take(T * k * (F / 32));
+    L.y_perm = take(T * k * d * 4);  // fp32 in the layer
+    L.total = off;
+    return L;
+}
+
+moe_status check_ws_mxfp4(const moe_problem* p, const void* ws, size_t ws_bytes)
+{
+    const size_t need = layout_mxfp4_of(p).total;
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+    return check_ptr(ws, "ws", 16);
+}
+
+// Rows of K values as MXFP4 codes.
+moe_status check_mxfp4_rows(int64_t rows, int32_t K, int32_t dtype)
+{
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "dtype=%d is neither MOE_F32 nor MOE_BF16", dtype);
+    if (rows < 0)
+        return fail(MOE_ERR_INVALID_ARG, "rows=%lld is negative", (long long)rows);
+    if (K < 32 || K > kMaxDim || K % 32)
+        return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 32 in [32, %d]", K, kMaxDim);
+    if (rows > ((long long)1 << 40) / K)
+        return fail(MOE_ERR_UNSUPPORTED, "too many rows");
+    return MOE_OK;
+}
+
+moe_status do_up_mxfp4(const moe_problem* p, const uint8_t* aq, const uint8_t* as, const int32_t* gather,
+                       const int32_t* offsets, const uint8_t* W1q, const uint8_t* w1s, uint8_t* hq, uint8_t* hs,
+                       float* partial, hipStream_t s)
+{
+    const int epi = p->act == MOE_ACT_SWIGLU ? 2 : 1;
+    return hip_status(moe_launch_mxfp4_gemm(epi, aq, as, gather, p->T, W1q, w1s, hq, hs, nullptr, offsets, p->E, p->d,
+                                            n1_of(p), p->F, p->F, p->T * p->k, mean_rows_of(p), cu_count(), partial,
+                                            s),
+                      "MXFP4 expert up launch");
+}
+
+moe_status do_down_mxfp4(const moe_problem* p, const uint8_t* hq, const uint8_t* hs, const int32_t* offsets,
+                         const uint8_t* W2q, const uint8_t* w2s, void* y_perm, bool f32, float* partial,
+                         hipStream_t s)
+{
+    return hip_status(moe_launch_mxfp4_gemm(f32 ? 3 : 0, hq, hs, nullptr, 0, W2q, w2s, nullptr, nullptr, y_perm,
+                                            offsets, p->E, p->F, p->d, p->d, p->F, p->T * p->k, mean_rows_of(p),
+                                            cu_count(), partial, s),
+                      "MXFP4 expert down launch");
+}
+
+// ---- orthogonalised updates
+moe_status check_orthogonalize(int32_t count, int32_t rows, int32_t cols)
+{
+    if (count < 0)
+        return fail(MOE_ERR_INVALID_ARG, "count=%d is negative", count);
+    if (rows < 1 || cols < 1)
+        return fail(MOE_ERR_INVALID_ARG, "rows=%d or cols=%d below 1", rows, cols);
+    if (rows > kMaxDim || cols > kMaxDim || count > kMaxMatrices)
+        return fail(MOE_ERR_UNSUPPORTED, "rows=%d or cols=%d above %d, or count=%d above %d", rows, cols, kMaxDim,
+                    count, kMaxMatrices);
+    if ((long long)rows * cols >= 1LL << 30 || (long long)count * rows * cols >= 1LL << 40)
+        return fail(MOE_ERR_UNSUPPORTED, "matrices of 2^30 values or more, or 2^40 values in all");
+    return MOE_OK;
 }
 
 // ---- backward
@@ -1192,6 +1314,183 @@ moe_status moe_forward_fp8_block(const moe_problem* p, const void* x, const void
     CHECK(do_down_fp8_block(p, hq, hs, offsets, W2q, w2s, w_scale, y_perm, true, partial, s));
     CHECK(hip_status(moe_launch_combine_rows(at<float>(ws, L.y_perm), slot, topk_w, p->T, p->d, p->k, p->T * p->k, y,
                                              s), "combine launch"));
+    return ok();
+}
+
+moe_status moe_quantize_mxfp4(const void* src, int32_t src_dtype, int64_t rows, int32_t K, uint8_t* codes,
+                              uint8_t* scales, void* stream)
+{
+    CHECK(check_mxfp4_rows(rows, K, src_dtype));
+    if (rows == 0)
+        return ok();
+    CHECK(check_ptr(src, "src", 16));
+    CHECK(check_ptr(codes, "codes", 16));
+    CHECK(check_ptr(scales, "scales", 1));
+    CHECK(hip_status(moe_launch_mxfp4_quantize(src_dtype == MOE_F32 ? 0 : 1, src, rows * (K / 32), codes, scales,
+                                               (hipStream_t)stream),
+                     "MXFP4 quantisation launch"));
+    return ok();
+}
+
+moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K, void* dst,
+                                int32_t dst_dtype, void* stream)
+{
+    CHECK(check_mxfp4_rows(rows, K, dst_dtype));
+    if (rows == 0)
+        return ok();
+    CHECK(check_ptr(codes, "codes", 16));
+    CHECK(check_ptr(scales, "scales", 1));
+    CHECK(check_ptr(dst, "dst", 16));
+    CHECK(hip_status(moe_launch_mxfp4_dequantize(dst_dtype == MOE_F32 ? 0 : 1, codes, scales, rows * (K / 32), dst,
+                                                 (hipStream_t)stream),
+                     "MXFP4 dequantisation launch"));
+    return ok();
+}
+
+moe_status moe_mxfp4_workspace_size(const moe_problem* p, size_t* bytes)
+{
+    CHECK(check_mxfp4(p));
+    if (!bytes)
+        return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = layout_mxfp4_of(p).total;
+    return ok();
+}
+
+moe_status moe_expert_up_mxfp4(const moe_problem* p, const uint8_t* aq, const uint8_t* as, const int32_t* src_token,
+                               const int32_t* offsets, const uint8_t* W1q, const uint8_t* w1s, uint8_t* hq,
+                               uint8_t* hs, void* ws, size_t ws_bytes, void* stream)
+{
+    CHECK(check_mxfp4(p));
+    if (p->T == 0)
+        return ok();
+    CHECK(check_ptr(aq, src_token ? "xq" : "x_perm codes", 16));
+    CHECK(check_ptr(as, "activation scales", 4));
+    if (src_token) {
+        CHECK(check_ptr(src_token, "src_token", 4));
+        if (!gather_ok_mxfp4(p))
+            return fail(MOE_ERR_UNSUPPORTED, "x codes of %llu bytes are too large to gather; pass permuted codes",
+                        (unsigned long long)p->T * (p->d / 2));
+    }
+    CHECK(check_ptr(offsets, "offsets", 4));
+    CHECK(check_ptr(W1q, "W1q", 16));
+    CHECK(check_ptr(w1s, "w1s", 4));
+    CHECK(check_ptr(hq, "hq", 16));
+    CHECK(check_ptr(hs, "hs", 4));
+    if (ws)
+        CHECK(check_ws_mxfp4(p, ws, ws_bytes));
+    float* partial = ws ? at<float>(ws, layout_mxfp4_of(p).partial) : nullptr;
+    CHECK(do_up_mxfp4(p, aq, as, src_token, offsets, W1q, w1s, hq, hs, partial, (hipStream_t)stream));
+    return ok();
+}
+
+moe_status moe_expert_down_mxfp4(const moe_problem* p, const uint8_t* hq, const uint8_t* hs, const int32_t* offsets,
+                                 const uint8_t* W2q, const uint8_t* w2s, void* y_perm, void* ws, size_t ws_bytes,
+                                 void* stream)
+{
+    CHECK(check_mxfp4(p));
+    if (p->T == 0)
+        return ok();
+    CHECK(check_ptr(hq, "hq", 16));
+    CHECK(check_ptr(hs, "hs", 4));
+    CHECK(check_ptr(offsets, "offsets", 4));
+    CHECK(check_ptr(W2q, "W2q", 16));
+    CHECK(check_ptr(w2s, "w2s", 4));
+    CHECK(check_ptr(y_perm, "y_perm", 16));
+    if (ws)
+        CHECK(check_ws_mxfp4(p, ws, ws_bytes));
+    float* partial = ws ? at<float>(ws, layout_mxfp4_of(p).partial) : nullptr;
+    CHECK(do_down_mxfp4(p, hq, hs, offsets, W2q, w2s, y_perm, false, partial, (hipStream_t)stream));
+    return ok();
+}
+
+moe_status moe_forward_mxfp4(const moe_problem* p, const void* x, const void* Wg, const float* bg, const uint8_t* W1q,
+                             const uint8_t* w1s, const uint8_t* W2q, const uint8_t* w2s, void* y, float* logits,
+                             const moe_route_info* info, void* ws, size_t ws_bytes, void* stream)
+{
+    CHECK(check_mxfp4(p));
+    if (p->T == 0)
+        return ok();
+    if (!gather_ok_mxfp4(p))
+        return fail(MOE_ERR_UNSUPPORTED, "x codes of %llu bytes are too large to gather (limit 0xF0000000 bytes)",
+                    (unsigned long long)p->T * (p->d / 2));
+    CHECK(check_ptr(w1s, "w1s", 4));
+    CHECK(check_ptr(w2s, "w2s", 4));
+    CHECK(check_forward(p, x, Wg, bg, W1q, W2q, y, logits));
+    CHECK(check_ws_mxfp4(p, ws, ws_bytes));
+    const LayoutMxfp4 L = layout_mxfp4_of(p);
+    moe_route_info r = {};
+    if (info)
+        r = *info;
+#define PICK(field, type) (r.field ? r.field : at<type>(ws, L.field))
+    int32_t* topk_idx = PICK(topk_idx, int32_t);
+    float* topk_w = PICK(topk_w, float);
+    int32_t* counts = PICK(counts, int32_t);
+    int32_t* offsets = PICK(offsets, int32_t);
+    int32_t* slot = PICK(slot, int32_t);
+    int32_t* src_token = PICK(src_token, int32_t);
+#undef PICK
+    const void* ptrs[] = {topk_idx, topk_w, counts, offsets, slot, src_token};
+    for (const void* q : ptrs)
+        CHECK(check_ptr(q, "route info field", 4));
+    float* z = logits ? logits : at<float>(ws, L.logits);
+    float* partial = at<float>(ws, L.partial);
+    uint8_t* xq = at<uint8_t>(ws, L.xq);
+    uint8_t* xs = at<uint8_t>(ws, L.xs);
+    uint8_t* hq = at<uint8_t>(ws, L.hq);
+    uint8_t* hs = at<uint8_t>(ws, L.hs);
+    void* y_perm = at<char>(ws, L.y_perm);
+    hipStream_t s = (hipStream_t)stream;
+    CHECK(do_route(p, Wg ? x : nullptr, Wg, bg, z, topk_idx, topk_w, s));
+    CHECK(hip_status(moe_launch_permute(p->dtype, topk_idx, x, p->T, p->d, p->E, p->k, capacity_of(p), counts,
+                                        offsets, slot, src_token, nullptr, at<int32_t>(ws, L.chunk_cnt), s),
+                     "permute launch"));
+    CHECK(hip_status(moe_launch_mxfp4_quantize(1, x, (long long)p->T * (p->d / 32), xq, xs, s),
+                     "MXFP4 quantisation launch"));
+    CHECK(do_up_mxfp4(p, xq, xs, src_token, offsets, W1q, w1s, hq, hs, partial, s));
+    CHECK(do_down_mxfp4(p, hq, hs, offsets, W2q, w2s, y_perm, true, partial, s));
+    CHECK(hip_status(moe_launch_combine_rows(at<float>(ws, L.y_perm), slot, topk_w, p->T, p->d, p->k, p->T * p->k, y,
+                                             s), "combine launch"));
+    return ok();
+}
+
+moe_status moe_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t cols, size_t* bytes)
+{
+    CHECK(check_orthogonalize(count, rows, cols));
+    if (!bytes)
+        return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = round_up(moe_orthogonalize_scratch_bytes(count, rows, cols));
+    return ok();
+}
+
+moe_status moe_orthogonalize(const void* grad, int32_t grad_dtype, float* momentum, float beta, int32_t nesterov,
+                             int32_t count, int32_t rows, int32_t cols, int32_t steps, void* out, void* ws,
+                             size_t ws_bytes, void* stream)
+{
+    CHECK(check_orthogonalize(count, rows, cols));
+    if (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "grad_dtype=%d is neither MOE_F32 nor MOE_BF16", grad_dtype);
+    if (nesterov != 0 && nesterov != 1)
+        return fail(MOE_ERR_INVALID_ARG, "nesterov=%d is neither 0 nor 1", nesterov);
+    if (nesterov && !momentum)
+        return fail(MOE_ERR_INVALID_ARG, "nesterov without a momentum");
+    if (momentum && !std::isfinite(beta))
+        return fail(MOE_ERR_INVALID_ARG, "beta must be finite");
+    if (steps < 1 || steps > kMaxSteps)
+        return fail(steps < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, "steps=%d outside [1, %d]", steps,
+                    kMaxSteps);
+    if (count == 0)
+        return ok();
+    CHECK(check_ptr(grad, "grad", grad_dtype == MOE_F32 ? 4 : 2));
+    if (momentum)
+        CHECK(check_ptr(momentum, "momentum", 4));
+    CHECK(check_ptr(out, "out", 2));
+    const size_t need = round_up(moe_orthogonalize_scratch_bytes(count, rows, cols));
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+    CHECK(check_ptr(ws, "ws", 16));
+    CHECK(hip_status(moe_launch_orthogonalize(grad_dtype == MOE_F32 ? 0 : 1, grad, momentum, beta, nesterov, count,
+                                              rows, cols, steps, out, ws, cu_count(), (hipStream_t)stream),
+                     "orthogonalising launch"));
     return ok();
 }
 
