@@ -10,6 +10,7 @@
 #include "common.h"
 #include "gemm_common.h"
 #include "mxfp4.h"
+#include "tile_gemm.h"
 
 namespace moe {
 
@@ -58,7 +59,43 @@ __global__ __launch_bounds__(256) void moe_mxfp4_dequantize_kernel(const uint8_t
 }
 
 // ---------------------------------------------------------------- grouped GEMM
+// Rows of expert e's segment times its weight matrix, in tiles of tile_gemm.h: a
+// slice is 256 values of K (128 bytes of codes and 8 scales of a row).  For SwiGLU the
+// two halves of a tile's weight rows are the gate rows and the matching up rows of
+// 128 hidden columns, else consecutive rows.
+//
+// MFMA 32x32x64 f8f6f4 with E2M1 operands: lane l holds 32 values (a block) of operand
+// row l % 32 and the byte that scales them, so the matrix core applies both scales of
+// a block itself.  The weight tile is its first operand, the activation tile its
+// second: a lane's accumulators are 4 consecutive columns of one row, and a 32 x 32
+// fragment holds whole blocks of h.
 enum { MXEPI_NONE = 0, MXEPI_RELU = 1, MXEPI_SWIGLU = 2, MXEPI_F32 = 3 };  // bf16 rows, hidden codes (2), fp32 rows
+
+constexpr int kMxSlice = 256;       // values of K of a slice
+constexpr int kMxMaxParts = 16;     // K parts of a tail tile
+constexpr int kMxSplitSlots = 256;  // partial tiles the workspace holds
+constexpr int kMxMinPart = 4;       // slices of a part
+
+typedef TileShape<256, 2, 4, 2, 8, 256, 1, true> LargeShape;
+typedef TileShape<128, 2, 4, 3, 8, 256, 1, true> Shape128;
+typedef TileShape<96, 1, 4, 3, 4, 256, 1, true> MediumShape;
+typedef TileShape<64, 1, 4, 3, 4, 256, 1, true> SmallShape;
+typedef TileShape<64, 2, 2, 3, 4, 128, 2, true> NarrowShape;
+
+// Experts that a shape's tile counts have room for: two blocks of NarrowShape share a
+// CU's 160 KB of LDS.
+template <typename S>
+constexpr int kMxMaxE = S::kPerCu > 1 ? 768 : kGemmMaxE;
+
+struct MxOp {
+    template <int BYTE>
+    static __device__ __forceinline__ f32x16 mma(const i32x4& w, const i32x4& a, const f32x16& c, int sw, int sa)
+    {
+        const i32x8 wv = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+        const i32x8 av = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 4, BYTE, sw, BYTE, sa);
+    }
+};
 
 struct MxGemmArgs {
     const uint8_t* A;       // codes of the activation rows [.][K / 2]
@@ -72,78 +109,325 @@ struct MxGemmArgs {
     void* Y;            // bf16 or fp32 rows [.][Nout] (plain epilogues)
     const int32_t* offsets;
     int E, K, Nw, Nout, F, max_rows;
+    float* partial;  // nullable: no K split
 };
 
-// One wavefront per 32 rows x 32 columns (SwiGLU: the gate and up rows of 32
-// hidden columns), fragments from memory.  MFMA 32x32x64 f8f6f4 with E2M1
-// operands: lane l holds block l / 32 of operand row l % 32 and its scale byte.
-struct MxTile {
-    static constexpr int BM = 32, GM = 8;
-};
-template <int EPI>
-__global__ __launch_bounds__(256) void moe_mxfp4_gemm_kernel(MxGemmArgs g)
+__device__ __forceinline__ int mx_parts(int total, int G, int nk, bool enabled)
 {
-#if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ int32_t s_pref[kGemmMaxE + 1];
-    __shared__ int32_t s_wsum[4];
+    const int tail = total % G;
+    if (!enabled || tail == 0)
+        return 1;
+    return max(1, min(min(kMxMaxParts, min(G, kMxSplitSlots) / tail), nk / kMxMinPart));
+}
+
+// silu(u) v, silu(u) = u / (1 + e^-u); the exponential and the reciprocal to within a
+// step or two of fp32, which the E2M1 code behind them does not see.
+__device__ __forceinline__ float mx_glu(float u, float v)
+{
+    return u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) * v;
+}
+
+// Hidden rows of row fragment i: every 32 x 32 fragment holds one block of each of its
+// rows, 16 of the values in lane l and 16 in lane l ^ 32, which are quantised as they
+// are (fp32, no rounding to bf16 in between).  The two lanes swap halves of their codes
+// so that each stores 8 consecutive bytes.
+template <typename S, int EPI>
+__device__ __forceinline__ void mx_store_hidden(const f32x16 (&acc)[S::kFN], int i, const TileDec& t,
+                                                const MxGemmArgs& g)
+{
+    constexpr bool kGlu = EPI == MXEPI_SWIGLU;
     const int lane = lane_id(), wave = threadIdx.x / kWave, half = lane >> 5;
-    const int ntn = (g.Nout + 31) / 32, nkb = g.K / kMxBlk;
-    tile_prefix<256>(g.offsets, g.E, g.max_rows, 32, ntn, s_pref, s_wsum);
-    const int total = s_pref[g.E];
-    for (int tile = blockIdx.x * 4 + wave; tile < total; tile += gridDim.x * 4) {
-        const TileDec t = decode_tile<MxTile>(tile, s_pref, g.offsets, g.E, g.max_rows, ntn, 32);
-        const int r = min(lane & 31, t.rows - 1);
-        int row = t.row0 + r;
-        if (g.gather)
-            row = min(max(g.gather[row], 0), g.gather_rows - 1);
-        const size_t n = (size_t)t.e * g.Nw + t.n0 + (lane & 31);
-        f32x16 acc[2] = {};
-        for (int b = half; b < nkb; b += 2) {
-            const uint4 a = *reinterpret_cast<const uint4*>(g.A + ((size_t)row * nkb + b) * 16);
-            const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-            const int as = g.As[(size_t)row * nkb + b];
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int m = wm * S::kWaveM + i * 32 + (lane & 31);
 #pragma unroll
-            for (int j = 0; j < (EPI == MXEPI_SWIGLU ? 2 : 1); ++j) {
-                const size_t at = (n + (size_t)j * g.F) * nkb + b;
-                const uint4 w = *reinterpret_cast<const uint4*>(g.W + at * 16);
-                const i32x8 wv = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-                acc[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, acc[j], 4, 4, 0, (int)g.Ws[at], 0, as);
-            }
-        }
+    for (int j = 0; j < (kGlu ? S::kHalfF : S::kFN); ++j) {
+        const int n = t.n0 + (j / S::kHalfF) * S::kHalf + wn * S::kHalfN + (j % S::kHalfF) * 32;
         float h[16];
         uint32_t amax = 0;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            const float u = acc[0][v];
-            h[v] = EPI == MXEPI_SWIGLU ? u / (1.0f + expf(-u)) * acc[1][v] : EPI == MXEPI_RELU && u <= 0.0f ? 0.0f : u;
+            const float u = acc[j][v];
+            if constexpr (kGlu)
+                h[v] = mx_glu(u, acc[j + S::kHalfF][v]);
+            else
+                h[v] = u <= 0.0f ? 0.0f : u;  // a NaN stays one
             amax = max(amax, abs_bits(h[v]));
         }
-        if constexpr (EPI == MXEPI_NONE || EPI == MXEPI_F32) {
-            if ((lane & 31) < t.rows)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const size_t at = (size_t)(t.row0 + r) * g.Nout + t.n0 + 8 * (v / 4) + 4 * half + v % 4;
-                    if constexpr (EPI == MXEPI_F32)
-                        static_cast<float*>(g.Y)[at] = h[v];
-                    else
-                        static_cast<uint16_t*>(g.Y)[at] = (uint16_t)f32_to_bf16_bits(h[v]);
-                }
-        } else {
-            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
-            const uint32_t s = mx_scale_byte(amax);
-            if ((lane & 31) < t.rows) {
-                const size_t out = (size_t)(t.row0 + r) * (g.Nout / kMxBlk) + t.n0 / kMxBlk;
-                const uint32_t lo = e2m1_encode8(h, s), hi = e2m1_encode8(h + 8, s);
-                uint16_t* dst = reinterpret_cast<uint16_t*>(g.Hq + out * 16) + half;
-                dst[0] = (uint16_t)lo;
-                dst[2] = (uint16_t)(lo >> 16);
-                dst[4] = (uint16_t)hi;
-                dst[6] = (uint16_t)(hi >> 16);
-                if (half == 0)
-                    g.Hs[out] = (uint8_t)s;
-            }
+        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
+        const uint32_t s = mx_scale_byte(amax);
+        // 16 bits of codes for each 4 columns 8 q + 4 half ..: this lane's of q = 0, 1 in
+        // c0, of q = 2, 3 in c1
+        const uint32_t c0 = e2m1_encode8(h, s), c1 = e2m1_encode8(h + 8, s);
+        const uint32_t got = (uint32_t)__shfl_xor((int)(half ? c0 : c1), 32), own = half ? c1 : c0;
+        const uint32_t lo = half ? got : own, hi = half ? own : got;  // of columns 8 q, and 8 q + 4
+        if (m < t.rows && n < g.Nout) {
+            const size_t at = (size_t)(t.row0 + m) * (g.Nout / kMxBlk) + n / kMxBlk;
+            *reinterpret_cast<uint2*>(g.Hq + at * 16 + 8 * half) =
+                make_uint2((lo & 0xffffu) | (hi << 16), (lo >> 16) | (hi & 0xffff0000u));
+            if (half == 0)
+                g.Hs[at] = (uint8_t)s;
         }
     }
+}
+
+// Plain rows of row fragment i of every wavefront (WM bands of 32 rows): staged in LDS
+// as [band row][column] (16-byte chunks XOR-swizzled by the row), then stored row by
+// row.
+template <typename S, int EPI>
+__device__ __forceinline__ void mx_store_rows(const f32x16 (&acc)[S::kFN], int i, const TileDec& t, uint8_t* buf,
+                                              const MxGemmArgs& g)
+{
+    constexpr int kEl = EPI == MXEPI_F32 ? 4 : 2;
+    constexpr int kRows = S::WM * 32, kRowBytes = S::BN * kEl;
+    constexpr int kSwz = kRowBytes / 16 - 1 < 31 ? kRowBytes / 16 - 1 : 31;
+    int tid = threadIdx.x;
+    __asm__ volatile("" : "+v"(tid));
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int r = wm * 32 + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int col = (j / S::kHalfF) * S::kHalf + wn * S::kHalfN + (j % S::kHalfF) * 32 + 8 * q + 4 * (lane >> 5);
+            const f32x4 v = {acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+            const int byte = col * kEl;
+            uint8_t* dst = buf + r * kRowBytes + (((byte >> 4) ^ (r & kSwz)) << 4) + (byte & 15);
+            if constexpr (kEl == 2) {
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<bf16x4*>(dst) = __builtin_convertvector(v, bf16x4);
+            } else {
+                *reinterpret_cast<f32x4*>(dst) = v;
+            }
+        }
+    lds_barrier();
+    constexpr int kChunks = kRowBytes / 16, kPer = 16 / kEl;
+#pragma unroll
+    for (int it = 0; it < kRows * kChunks / S::kThreads; ++it) {
+        const int c = tid + it * S::kThreads;
+        const int rr = c / kChunks, q = c % kChunks;
+        const int m = (rr / 32) * S::kWaveM + i * 32 + (rr % 32);
+        if (m < t.rows && t.n0 + q * kPer < g.Nout)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.Y) +
+                                      ((size_t)(t.row0 + m) * g.Nout + t.n0 + q * kPer) * kEl) =
+                *reinterpret_cast<const uint4*>(buf + rr * kRowBytes + ((q ^ (rr & kSwz)) << 4));
+    }
+}
+
+template <typename S, int EPI>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
+void moe_mxfp4_gemm_kernel(MxGemmArgs g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)  // the body uses device-only types; the host pass needs the stub only
+    static_assert(2 * (S::WM * 32) * S::BN * 4 <= S::S * S::kStage, "two staged row fragments fit the stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
+    __shared__ int32_t s_pref[kMxMaxE<S> + 1];
+    __shared__ int32_t s_wsum[S::kWaves];
+    const int tid = threadIdx.x;
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int pitch = g.K / 2, spitch = g.K / kMxBlk;  // bytes of a row's codes and scales
+    const int nk = (g.K + kMxSlice - 1) / kMxSlice;
+    const int ragged = g.K % kMxSlice ? nk - 1 : -1;  // the slice of which only the first half is there
+    const uint32_t lds0 = lds_addr(lds);
+
+    const int tile_cols = EPI == MXEPI_SWIGLU ? S::kHalf : S::BN;
+    const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
+    const int total = s_pref[g.E];
+    const int G = gridDim.x;
+    const int parts = mx_parts(total, G, nk, g.partial != nullptr);
+    const int full = parts > 1 ? total - total % G : total;
+    const int tail = total - full;
+    const int items = full + tail * parts;
+
+    for (int base = 0; base < items; base += G) {
+        const int b = blockIdx.x;
+        // an XCD's blocks side by side; with two blocks a CU a round that is not full
+        // is spread over all XCDs
+        const int each = S::kPerCu > 1 ? (min(G, items - base) + 7) / 8 : G / 8;
+        const int item = (G % 8 == 0) ? base + (b % 8) * each + b / 8 : base + b;
+        if (item >= items || (S::kPerCu > 1 && G % 8 == 0 && b / 8 >= each))
+            continue;
+        int tile = item, k0 = 0, k1 = nk, slot = -1;
+        if (item >= full) {
+            const int j = item - full, part = j / tail;
+            tile = full + j % tail;
+            k0 = part * nk / parts;
+            k1 = (part + 1) * nk / parts;
+            slot = (j % tail) * parts + part;
+        }
+        const TileDec t = decode_tile<S>(tile, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
+
+        // lane's place in a 1 KB load of kRows rows: row lane / 8, physical chunk
+        // lane % 8; the swizzle term is the same in all of a wavefront's loads (their
+        // row blocks all have the parity of its number)
+        const int lrow = S::kRows * wave + lane / 8;
+        const int chunk = (lane % 8) ^ tile_swz(lrow);
+        const uint32_t lchunk = (uint32_t)chunk * 16;
+        // the second half of a ragged slice reads behind the buffer: zeros
+        const uint32_t cutA = chunk >= 4 ? 0xf0000000u : 0;
+        // first rows of the two halves of the weight tile; the second, or its end, may
+        // lie behind the matrix
+        const uint32_t half1 = EPI == MXEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + S::kHalf);
+        const bool second = EPI == MXEPI_SWIGLU || (int)half1 < g.Nw;
+        uint32_t voffA[S::kBlkA];
+        auto source = [&](int r) {  // the row of A of tile row r, -1 for none
+            if (r >= t.rows)
+                return -1;
+            if (!g.gather)
+                return r;
+            const int src = g.gather[t.row0 + r];
+            return src < g.gather_rows ? src : -1;
+        };
+        const size_t rowA = g.gather ? 0 : t.row0;
+        const uint32_t rowsA = g.gather ? g.gather_rows : t.rows;
+        const i32x4 rsA = make_rsrc(g.A + rowA * pitch, rowsA * (uint32_t)pitch);
+#pragma unroll
+        for (int i = 0; i < S::kBlkA; ++i) {
+            const int src = source(lrow + S::kRows * S::kWaves * i);
+            voffA[i] = src >= 0 ? (uint32_t)src * (uint32_t)pitch + lchunk : 0xf0000000u;
+        }
+        const i32x4 rsW = make_rsrc(g.W + (size_t)t.e * g.Nw * pitch, (uint32_t)g.Nw * (uint32_t)pitch);
+        const uint32_t voffW = (uint32_t)lrow * (uint32_t)pitch + lchunk;
+        const uint32_t voffW1 = second ? voffW : 0xf0000000u, row0 = (uint32_t)t.n0 * (uint32_t)pitch;
+        const uint32_t row1 = second ? half1 * (uint32_t)pitch : 0, step = S::kRows * S::kWaves * (uint32_t)pitch;
+        // scale groups of this wavefront, the two dwords of 32 rows each, A's rows first;
+        // where they do not come out even, a wavefront repeats another's load
+        uint32_t voffS[S::kBlkS];
+        i32x4 rsS[S::kBlkS];
+        const uint32_t cutS = lane & 1 ? 0xf0000000u : 0;
+#pragma unroll
+        for (int q = 0; q < S::kBlkS; ++q) {
+            const int group = (wave + q * S::kWaves) % S::kSclGroups;
+            const int r = group * 32 + lane / 2 - (group < S::kSclGroupsA ? 0 : S::BM);
+            const bool a = group < S::kSclGroupsA;
+            const uint8_t* base = a ? g.As + rowA * spitch : g.Ws + (size_t)t.e * g.Nw * spitch;
+            rsS[q] = make_rsrc(base, (a ? rowsA : (uint32_t)g.Nw) * (uint32_t)spitch);
+            int src = a ? source(r) : r < S::kHalf ? t.n0 + r : (int)half1 + r - S::kHalf;
+            if (!a && src >= g.Nw)
+                src = -1;
+            voffS[q] = src >= 0 ? (uint32_t)src * (uint32_t)spitch + 4 * (lane & 1) : 0xf0000000u;
+        }
+        // Small tiles, which stream weights: every tile of columns starts at another
+        // slice, so that blocks which read rows a power of two apart at a time do not
+        // meet in few of the memory's channels.  The tile decides, so the sums keep
+        // their order from run to run.
+        constexpr bool kRotate = S::kWaves == 4;
+        int rot = 0;
+        if (kRotate && pitch >= 4096 && pitch % 2048 == 0)
+            rot = (t.n0 / tile_cols * 5) % (k1 - k0);
+
+        auto issue = [&](int q, int st, int n0, int n1) {
+            const uint32_t at = lds0 + st * S::kStage, dst = at + wave * 1024;
+            int kb = q;
+            if constexpr (kRotate)
+                kb = q + rot >= k1 ? q + rot - (k1 - k0) : q + rot;
+            const uint32_t soff = (uint32_t)kb * S::RB, cut = kb == ragged ? 0xffffffffu : 0;
+#pragma unroll
+            for (int p = 0; p < S::kLoads; ++p) {
+                if (p < n0 || p >= n1)
+                    continue;
+                if (p < S::kBlkW / 2)
+                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW, soff + row0 + p * step);
+                else if (p < S::kBlkW)
+                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == MXEPI_SWIGLU ? voffW : voffW1,
+                          soff + row1 + (p - S::kBlkW / 2) * step);
+                else if (p < S::kBlkW + S::kBlkS) {
+                    const int s = p - S::kBlkW;
+                    dma4(rsS[s], at + S::kLdsA + S::kLdsW + (wave + s * S::kWaves) % S::kSclGroups * 256,
+                         voffS[s] | (cutS & cut), (uint32_t)kb * 8);
+                } else {
+                    const int a = p - S::kBlkW - S::kBlkS;
+                    dma16(rsA, dst + S::kWaves * a * 1024, voffA[a] | (cutA & cut), soff);
+                }
+            }
+        };
+
+        wait_vmcnt<0>();  // the previous tile's stores are out of the count
+        __syncthreads();  // and every wave is done with its LDS
+        f32x16 acc[S::kFM][S::kFN];
+        const int live = min(max((t.rows - wm * S::kWaveM + 31) / 32, 0), S::kFM);
+        tile_product<S, MxOp>(acc, lds, wm, wn, live, k0, k1, issue);
+        if (slot < 0) {
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i) {
+                if constexpr (EPI == MXEPI_NONE || EPI == MXEPI_F32) {
+                    if (i * 32 < t.rows)
+                        mx_store_rows<S, EPI>(acc[i], i, t, lds + (i & 1) * (S::WM * 32 * S::BN * 4), g);
+                } else if (i < live) {
+                    mx_store_hidden<S, EPI>(acc[i], i, t, g);
+                }
+            }
+        } else {
+            // rows past the segment's end stay unwritten
+            float* dst = g.partial + (size_t)slot * S::kTileFloats;
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i)
+                if (wm * S::kWaveM + i * 32 + (lane & 31) < t.rows)
+#pragma unroll
+                    for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<float4*>(
+                                dst + ((((size_t)i * S::kWaves + wave) * S::kFN + j) * 4 + q) * 256 + lane * 4) =
+                                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                            acc[i][j][4 * q + 3]);
+        }
+    }
+#endif
+}
+
+// Second pass of the K split: block (split tile, row fragment) adds the parts in part
+// order and runs the epilogue.
+template <typename S, int EPI>
+__global__ __launch_bounds__(S::kThreads) void moe_mxfp4_tail_kernel(MxGemmArgs g, int G)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) uint8_t buf[S::WM * 32 * S::BN * 4];
+    __shared__ int32_t s_pref[kGemmMaxE + 1];
+    __shared__ int32_t s_wsum[S::kWaves];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int tile_cols = EPI == MXEPI_SWIGLU ? S::kHalf : S::BN;
+    const int ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    tile_prefix<S::kThreads>(g.offsets, g.E, g.max_rows, S::BM, ntn, s_pref, s_wsum);
+    const int total = s_pref[g.E];
+    const int parts = mx_parts(total, G, (g.K + kMxSlice - 1) / kMxSlice, true);
+    if (parts <= 1)
+        return;
+    const int tail = total % G, full = total - tail;
+    const int j = blockIdx.x / S::kFM, i = blockIdx.x % S::kFM;
+    if (j >= tail)
+        return;
+    const TileDec t = decode_tile<S>(full + j, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
+    if (i * 32 >= t.rows)
+        return;
+    const bool live = (wave / S::WN) * S::kWaveM + i * 32 + (lane & 31) < t.rows;
+    f32x16 acc[S::kFN];
+#pragma unroll
+    for (int n = 0; n < S::kFN; ++n)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            acc[n][v] = 0.0f;
+    for (int part = 0; live && part < parts; ++part) {
+        const float* src = g.partial + (size_t)(j * parts + part) * S::kTileFloats +
+                           (size_t)(i * S::kWaves + wave) * S::kFN * 1024 + lane * 4;
+#pragma unroll
+        for (int n = 0; n < S::kFN; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 p = *reinterpret_cast<const float4*>(src + (n * 4 + q) * 256);
+                acc[n][4 * q] += p.x;
+                acc[n][4 * q + 1] += p.y;
+                acc[n][4 * q + 2] += p.z;
+                acc[n][4 * q + 3] += p.w;
+            }
+    }
+    if constexpr (EPI == MXEPI_NONE || EPI == MXEPI_F32)
+        mx_store_rows<S, EPI>(acc, i, t, buf, g);
+    else
+        mx_store_hidden<S, EPI>(acc, i, t, g);
 #endif
 }
 
@@ -151,6 +435,71 @@ __global__ __launch_bounds__(256) void moe_mxfp4_gemm_kernel(MxGemmArgs g)
 
 namespace {
 using namespace moe;
+
+constexpr int kLargeRows = 192;
+
+// Whether the last round (at most kMxSplitSlots / 2 tiles of it) is split along K.  The
+// split costs a second launch (about 4 us), so it is left out where K is short, and
+// where the tiles expected (rows spread evenly over min(rows, E) experts) fill more
+// than half of the only round.
+template <typename S>
+bool split_pays(const MxGemmArgs& g, long long ntn, int blocks)
+{
+    if (g.K < 4096)
+        return false;
+    const long long busy = std::min(g.E, g.max_rows);
+    const long long tiles = busy * std::max(1ll, (g.max_rows / busy + S::BM - 1) / S::BM) * ntn;
+    return tiles <= std::min(blocks, kMxSplitSlots) / 2 || tiles > blocks;
+}
+
+bool narrow_pays(int mean_rows, long long tiles, int K, int ncu)
+{
+    if (tiles <= ncu)
+        return true;
+    if (mean_rows >= kLargeRows)
+        return tiles <= 2 * ncu;
+    if (K < 4096)
+        return mean_rows <= 32 || tiles <= 2 * ncu;
+    return false;
+}
+
+template <typename S, int EPI>
+hipError_t launch_shape(MxGemmArgs g, int ncu, hipStream_t stream)
+{
+    const int tile_cols = EPI == MXEPI_SWIGLU ? S::kHalf : S::BN;
+    const long long ntn = (g.Nout + tile_cols - 1) / tile_cols;
+    // upper bound on m-tiles: whole tiles plus one partial per expert
+    const long long mt = g.max_rows / S::BM + (long long)std::min(g.E, g.max_rows);
+    ncu *= S::kPerCu;
+    if (!split_pays<S>(g, ntn, ncu))
+        g.partial = nullptr;
+    long long grid = ncu;
+    if (mt * ntn < grid && g.partial == nullptr)
+        grid = (mt * ntn + 7) / 8 * 8;
+    moe_mxfp4_gemm_kernel<S, EPI><<<dim3((unsigned)grid), dim3(S::kThreads), 0, stream>>>(g);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || g.partial == nullptr)
+        return err;
+    moe_mxfp4_tail_kernel<S, EPI>
+        <<<dim3(kMxSplitSlots / 2 * S::kFM), dim3(S::kThreads), 0, stream>>>(g, (int)grid);
+    return hipGetLastError();
+}
+
+template <typename S>
+hipError_t launch_narrow(int epi, const MxGemmArgs& g, int ncu, hipStream_t s)
+{
+    if (epi == MXEPI_RELU)
+        return launch_shape<S, MXEPI_RELU>(g, ncu, s);
+    return epi == MXEPI_F32 ? launch_shape<S, MXEPI_F32>(g, ncu, s) : launch_shape<S, MXEPI_NONE>(g, ncu, s);
+}
+
+template <typename S>
+hipError_t launch_epi(int epi, const MxGemmArgs& g, int ncu, hipStream_t s)
+{
+    if (epi == MXEPI_SWIGLU)
+        return launch_shape<S, MXEPI_SWIGLU>(g, ncu, s);
+    return launch_narrow<S>(epi, g, ncu, s);
+}
 
 template <typename ET>
 void launch_quantize(const void* src, long long blocks, uint8_t* codes, uint8_t* scales, hipStream_t s)
@@ -199,25 +548,35 @@ extern "C" hipError_t moe_launch_mxfp4_dequantize(int dtype, const uint8_t* code
 // Bytes of the K split's partial tiles for this mean number of rows per expert.
 extern "C" size_t moe_mxfp4_gemm_partial_bytes(int mean_rows)
 {
-    return 0;
+    return (size_t)kMxSplitSlots * 4 * (mean_rows >= kLargeRows ? LargeShape::kTileFloats : MediumShape::kTileFloats);
 }
 
-// epi 0: Y = bf16 rows, 3: Y = fp32 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.
+// epi 0: Y = bf16 rows, 3: Y = fp32 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  mean_rows:
+// expected rows per expert.  partial (nullable): the K split's workspace,
+// moe_mxfp4_gemm_partial_bytes bytes.
 extern "C" hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uint8_t* As, const int32_t* gather,
                                             int gather_rows, const uint8_t* W, const uint8_t* Ws, uint8_t* Hq,
                                             uint8_t* Hs, void* Y, const int32_t* offsets, int E, int K, int Nw,
                                             int Nout, int F, int max_rows, int mean_rows, int ncu, float* partial,
                                             hipStream_t stream)
 {
-    const MxGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F, max_rows};
-    const dim3 grid(4 * ncu), block(256);
-    if (epi == MXEPI_NONE)
-        moe_mxfp4_gemm_kernel<MXEPI_NONE><<<grid, block, 0, stream>>>(g);
-    else if (epi == MXEPI_RELU)
-        moe_mxfp4_gemm_kernel<MXEPI_RELU><<<grid, block, 0, stream>>>(g);
-    else if (epi == MXEPI_SWIGLU)
-        moe_mxfp4_gemm_kernel<MXEPI_SWIGLU><<<grid, block, 0, stream>>>(g);
-    else
-        moe_mxfp4_gemm_kernel<MXEPI_F32><<<grid, block, 0, stream>>>(g);
-    return hipGetLastError();
+    const MxGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F,
+                          max_rows, partial};
+    const long long narrow = (long long)std::min(E, max_rows) * std::max(1, (mean_rows + 63) / 64) * (Nout / 128);
+    if (epi != MXEPI_SWIGLU && E <= kMxMaxE<NarrowShape> && narrow_pays(mean_rows, narrow, K, ncu))
+        return launch_narrow<NarrowShape>(epi, g, ncu, stream);
+    const int tile_cols = epi == MXEPI_SWIGLU ? 128 : 256;
+    const long long ntn = (Nout + tile_cols - 1) / tile_cols, busy = std::min(E, max_rows);
+    if (mean_rows >= kLargeRows) {
+        auto most = [&](int bm) { return (busy == 1 ? (max_rows + bm - 1) / bm : max_rows / bm + busy) * ntn; };
+        if (most(MediumShape::BM) <= ncu)
+            return launch_epi<MediumShape>(epi, g, ncu, stream);
+        if (most(Shape128::BM) <= ncu)
+            return launch_epi<Shape128>(epi, g, ncu, stream);
+        return launch_epi<LargeShape>(epi, g, ncu, stream);
+    }
+    const long long tiles = busy * ((mean_rows + 95) / 96 + (mean_rows == 0)) * ntn;
+    if (tiles < ncu)
+        return launch_epi<SmallShape>(epi, g, ncu, stream);
+    return launch_epi<MediumShape>(epi, g, ncu, stream);
 }
