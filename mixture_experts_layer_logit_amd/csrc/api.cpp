@@ -79,7 +79,7 @@ hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uint8_t* As, c
                                  int mean_rows, int ncu, float* partial, hipStream_t stream);
 size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols);
 hipError_t moe_launch_orthogonalize(int dtype, const void* grad, float* momentum, float beta, int nesterov, int count,
-                                    int rows, int cols, int steps, void* out, void* ws, int ncu, hipStream_t stream);
+                                    int rows, int cols, int steps, void* out, void* ws, hipStream_t stream);
 size_t moe_balance_scratch_bytes(void);
 hipError_t moe_launch_balance(const float* logits, const int32_t* topk_idx, const int32_t* offsets, int S, int T,
                               int E, int k, int normalize, float lambda, float aux_coef, float z_coef,
@@ -1489,7 +1489,7 @@ moe_status moe_orthogonalize(const void* grad, int32_t grad_dtype, float* moment
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
     CHECK(check_ptr(ws, "ws", 16));
     CHECK(hip_status(moe_launch_orthogonalize(grad_dtype == MOE_F32 ? 0 : 1, grad, momentum, beta, nesterov, count,
-                                              rows, cols, steps, out, ws, cu_count(), (hipStream_t)stream),
+                                              rows, cols, steps, out, ws, (hipStream_t)stream),
                      "orthogonalising launch"));
     return ok();
 }

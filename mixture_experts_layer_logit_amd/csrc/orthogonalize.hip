@@ -12,13 +12,13 @@
 // leaves fp16's normal range (singular values stay below 1.21, the entries of A
 // below 1.5, those of B below 2.9).  A small singular value grows by a = 3.44 a step,
 // and with it every rounding that lands on its vectors.  Two of them are kept off:
-//   * a X is added from an fp32 X (rounded to fp16 it put the result of a gradient
-//     of low rank 2e-2 off, now 5e-4);
+//   * a X is added from an X of 22 bits, an fp16 number and an fp16 remainder (rounded
+//     to fp16 it put the result of a gradient of low rank 2e-2 off, now 5e-4);
 //   * the diagonals of A and B, which outweigh the rest of their rows, stay in
 //     fp32: X' = a X + diag(B) X + offdiag(B) X.  In the second term X is the fp16
 //     operand, so that the rounding of X meets one B as a whole, whose product with
 //     it is small where A is; in the last two steps, whose errors no longer grow,
-//     it is the fp32 X (Gaussian 512 x 1024: 1.6e-3 -> 7e-4).
+//     it is the whole X (Gaussian 512 x 1024: 1.6e-3 -> 7e-4).
 // With bf16 iterates the same gradients are 1e-2 to 2e-1 off.
 #include <algorithm>
 #include <cmath>
@@ -29,66 +29,118 @@
 
 namespace moe {
 
-constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
-constexpr float kNsScale = 16384.0f;  // of the fp16 A and B
-constexpr int kNsPad = 64;            // rows of fp16 operands are padded to whole slices
-constexpr int kNsSums = 256;          // partial sums of squares of a matrix, at most
+[[maybe_unused]] constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+[[maybe_unused]] constexpr float kNsScale = 16384.0f;  // of the fp16 A and B
+[[maybe_unused]] constexpr float kNsLow = 2048.0f;     // of the remainder of X: fp16 keeps 11 bits before it
+constexpr int kNsPad = 64;    // rows of fp16 operands are padded to whole slices
+constexpr int kNsSums = 512;  // partial sums of squares of a matrix, at most
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-// One batch: matrices of m x n (m <= n), X^T where the source is tall.
+// One batch: X of m x n (m <= n), which is U, or U^T where the source is tall.
 struct NsArgs {
     const void* grad;
     float* momentum;  // nullable
     uint16_t* out;    // bf16
-    _Float16* x;      // [count][m][np], scaled by sx
-    _Float16* xt;     // [2][count][n][mp]
-    float* x32;       // [count][np / 32][mp / 32] fragments of X^T, see ns_frag
-    _Float16* a;      // [count][m][mp], scaled by kNsScale, zero diagonal
-    _Float16* b;      // [count][m][mp]
+    _Float16* x;      // [count][m][np] X, scaled by sx
+    _Float16* xt;     // [2][count][n][mp] X^T, scaled by sx
+    _Float16* low;    // [count][np / 32][mp / 32] fragments of the remainder of X^T, scaled by sx kNsLow, see ns_frag
+    _Float16* a;      // [count][m][mp] A, scaled by kNsScale, zero diagonal
+    _Float16* b;      // [count][m][mp] B, the same
     float* da;        // [count][mp] diagonal of A
     float* db;        // [count][mp] of B
     double* sums;     // [count][kNsSums]
+    float* partial;   // partial tiles of split products
     float beta, sx;
     int src_dtype, nesterov, count, rows, cols, m, n, mp, np, parts;
+    bool vec;  // four neighbouring values of the sources can be loaded at once
 };
 
-__device__ __forceinline__ float ns_grad(const NsArgs& g, size_t at)
+// Four values of the gradient from element `at` on, of which the first `held` are there.
+__device__ __forceinline__ f32x4 ns_load_grad(const NsArgs& g, size_t at, int held)
 {
-    return g.src_dtype == 0 ? static_cast<const float*>(g.grad)[at]
-                            : bf16_bits_to_f32(static_cast<const uint16_t*>(g.grad)[at]);
+    f32x4 v = {0, 0, 0, 0};
+    if (g.src_dtype == 0) {
+        const float* p = static_cast<const float*>(g.grad) + at;
+        if (g.vec && held == 4)
+            return *reinterpret_cast<const f32x4*>(p);
+        for (int q = 0; q < held; ++q)
+            v[q] = p[q];
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(g.grad) + at;
+        if (g.vec && held == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                         __uint_as_float(w.y & 0xffff0000u)};
+        }
+        for (int q = 0; q < held; ++q)
+            v[q] = bf16_bits_to_f32(p[q]);
+    }
+    return v;
 }
 
-// U at an element, from the gradient and the momentum of this step.
-__device__ __forceinline__ float ns_update(const NsArgs& g, size_t at)
+__device__ __forceinline__ f32x4 ns_load_momentum(const NsArgs& g, size_t at, int held)
+{
+    const float* p = g.momentum + at;
+    if (g.vec && held == 4)
+        return *reinterpret_cast<const f32x4*>(p);
+    f32x4 v = {0, 0, 0, 0};
+    for (int q = 0; q < held; ++q)
+        v[q] = p[q];
+    return v;
+}
+
+// Four values of U once the momentum is this step's.
+__device__ __forceinline__ f32x4 ns_load_update(const NsArgs& g, size_t at, int held)
 {
     if (!g.momentum)
-        return ns_grad(g, at);
-    return g.nesterov ? fmaf(g.beta, g.momentum[at], ns_grad(g, at)) : g.momentum[at];
+        return ns_load_grad(g, at, held);
+    f32x4 m = ns_load_momentum(g, at, held);
+    if (g.nesterov) {
+        const f32x4 v = ns_load_grad(g, at, held);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            m[q] = fmaf(g.beta, m[q], v[q]);
+    }
+    return m;
 }
 
-// Momentum, and sums of squares of U in fp64: block (part, matrix).
+// Momentum and sums of squares of U in fp64: block (part, matrix).
 __global__ __launch_bounds__(256) void moe_ns_sums_kernel(NsArgs g)
 {
-    __shared__ double s_sum[256];
+    __shared__ double s_sum[4];
     const size_t each = (size_t)g.rows * g.cols, base = (size_t)blockIdx.y * each;
     double sum = 0.0;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < each; i += (size_t)g.parts * 256) {
-        if (g.momentum)
-            g.momentum[base + i] = fmaf(g.beta, g.momentum[base + i], ns_grad(g, base + i));
-        const double u = ns_update(g, base + i);
-        sum += u * u;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < each; i += (size_t)g.parts * 1024) {
+        const int held = (int)min((size_t)4, each - i);
+        f32x4 u = ns_load_grad(g, base + i, held);
+        if (g.momentum) {
+            f32x4 m = ns_load_momentum(g, base + i, held);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                m[q] = fmaf(g.beta, m[q], u[q]);
+                u[q] = g.nesterov ? fmaf(g.beta, m[q], u[q]) : m[q];
+            }
+            float* p = g.momentum + base + i;
+            if (g.vec && held == 4)
+                *reinterpret_cast<f32x4*>(p) = m;
+            else
+                for (int q = 0; q < held; ++q)
+                    p[q] = m[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sum += (double)u[q] * u[q];
     }
-    s_sum[threadIdx.x] = sum;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        sum += __shfl_xor(sum, o);
+    if (lane_id() == 0)
+        s_sum[threadIdx.x / kWave] = sum;
     __syncthreads();
-    for (int o = 128; o >= 1; o >>= 1) {
-        if ((int)threadIdx.x < o)
-            s_sum[threadIdx.x] += s_sum[threadIdx.x + o];
-        __syncthreads();
-    }
     if (threadIdx.x == 0)
-        g.sums[(size_t)blockIdx.y * kNsSums + blockIdx.x] = s_sum[0];
+        g.sums[(size_t)blockIdx.y * kNsSums + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
 }
 
 // First value of the 32 x 32 fragment of X^T at row 32 fi, column 32 fj: 4 groups of
@@ -99,56 +151,81 @@ __device__ __forceinline__ size_t ns_frag(const NsArgs& g, size_t mat, int fi, i
     return ((mat * (g.np / 32) + fi) * (g.mp / 32) + fj) * 1024;
 }
 
-// X = U / |U|_F in both orientations, and the padding of every operand: block
-// (tile of 32 x 32 of the padded X, matrix).
+// X = U / |U|_F in all its forms: block (64 x 64 of the padded X, matrix).
 __global__ __launch_bounds__(256) void moe_ns_init_kernel(NsArgs g)
 {
-    __shared__ float tile[32][33];
-    const int tn = g.np / 32;
-    const int i0 = blockIdx.x / tn * 32, j0 = blockIdx.x % tn * 32;
-    const size_t mat = blockIdx.y;
-    double sum = 0.0;
-    for (int p = 0; p < g.parts; ++p)
-        sum += g.sums[mat * kNsSums + p];
-    // 1 / |U|: U is zero where the sum is
-    const double inv = sum > 0.0 || sum != sum ? 1.0 / sqrt(sum) : 0.0;
-    const size_t base = mat * g.rows * g.cols;
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    __shared__ float tile[64][65];
+    __shared__ double s_sum[4];
+    const int tn = g.np / 64, tid = threadIdx.x, lane = lane_id();
+    const int i0 = blockIdx.x / tn * 64, j0 = blockIdx.x % tn * 64;
+    const size_t mat = blockIdx.y, base = mat * g.rows * g.cols;
     const bool tall = g.rows > g.cols;
+    const int r0 = tall ? j0 : i0, c0 = tall ? i0 : j0;  // of the source
+    f32x4 u[4];
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-        const int u = ty + k;  // source rows one after another
-        const int i = tall ? i0 + tx : i0 + u, j = tall ? j0 + u : j0 + tx;
-        float v = 0.0f;
-        if (i < g.m && j < g.n)
-            v = (float)(ns_update(g, base + (tall ? (size_t)j * g.cols + i : (size_t)i * g.cols + j)) * inv);
-        tile[tall ? tx : u][tall ? u : tx] = v;
+    for (int k = 0; k < 4; ++k) {
+        const int r = r0 + tid / 16 + 16 * k, c = c0 + tid % 16 * 4;
+        u[k] = f32x4{0, 0, 0, 0};
+        if (r < g.rows && c < g.cols)
+            u[k] = ns_load_update(g, base + (size_t)r * g.cols + c, min(4, g.cols - c));
     }
+    double sum = 0.0;
+    for (int p = tid; p < g.parts; p += 256)
+        sum += g.sums[mat * kNsSums + p];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        sum += __shfl_xor(sum, o);
+    if (lane == 0)
+        s_sum[tid / kWave] = sum;
     __syncthreads();
-    const size_t cells = (size_t)g.count * g.n * g.mp;
-    float* frag = g.x32 + ns_frag(g, mat, j0 / 32, i0 / 32);
+    sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+    // zeros stay zeros; a NaN or an infinity anywhere makes the matrix NaN
+    const double inv = sum == 0.0 ? 0.0 : sum * 0.0 + g.sx / sqrt(sum);
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-        int i = i0 + ty + k, j = j0 + tx;
-        if (i < g.m)
-            g.x[(mat * g.m + i) * g.np + j] = (_Float16)(tile[ty + k][tx] * g.sx);
-        i = i0 + tx, j = j0 + ty + k;
-        const float v = tile[tx][ty + k];
-        frag[((tx / 8) * 64 + (tx / 4 % 2) * 32 + ty + k) * 4 + tx % 4] = v;
-        if (j < g.n) {
-            const size_t at = (mat * g.n + j) * g.mp + i;
-            g.xt[at] = (_Float16)(v * g.sx);
-            if (i >= g.m)
-                g.xt[cells + at] = (_Float16)0.0f;
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = tid / 16 + 16 * k, c = tid % 16 * 4 + q;
+            tile[tall ? c : r][tall ? r : c] = (float)(u[k][q] * inv);
         }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = tid / 8 + 32 * k, c = tid % 8 * 8;
+        f16x8 v, w;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            v[q] = (_Float16)tile[r][c + q];
+            w[q] = (_Float16)tile[c + q][r];
+        }
+        if (i0 + r < g.m)
+            *reinterpret_cast<f16x8*>(g.x + (mat * g.m + i0 + r) * g.np + j0 + c) = v;
+        if (j0 + r < g.n)
+            *reinterpret_cast<f16x8*>(g.xt + (mat * g.n + j0 + r) * g.mp + i0 + c) = w;
     }
-    if (j0 == 0 && threadIdx.x < 32) {
-        g.da[mat * g.mp + i0 + threadIdx.x] = 0.0f;
-        g.db[mat * g.mp + i0 + threadIdx.x] = 0.0f;
+    const int fi = tid / 128, fj = tid / 64 % 2;
+    _Float16* low = g.low + ns_frag(g, mat, j0 / 32 + fi, i0 / 32 + fj);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f16x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = tile[fj * 32 + 8 * q + 4 * (lane >> 5) + e][fi * 32 + (lane & 31)];
+            v[e] = (_Float16)((f - (float)(_Float16)f) * kNsLow);
+        }
+        *reinterpret_cast<f16x4*>(low + q * 256 + lane * 4) = v;
+    }
+    if (j0 == 0 && tid < 64) {
+        g.da[mat * g.mp + i0 + tid] = 0.0f;
+        g.db[mat * g.mp + i0 + tid] = 0.0f;
     }
 }
 
 // ---------------------------------------------------------------- the products
+// One output tile of a product per block:
+//   GRAM    A = X X^T      POLY    B = b A + c A^2      UPDATE    X^T <- a X^T + X^T B
+// A and B are symmetric: only tiles on and below the diagonal are computed, and stored
+// on both sides of it.
 enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
 struct NsOp {
@@ -162,6 +239,19 @@ struct NsOp {
 
 typedef TileShape<256, 2, 4, 2, 4, 256, 1, false> NsLarge;
 typedef TileShape<128, 2, 2, 2, 8, 128, 2, false> NsSmall;
+
+// The tiles of a product: `full` of them in one piece, the others, fewer than blocks run
+// at a time, in `parts` parts along K, whose sums moe_ns_tail_kernel adds.
+struct NsPlan {
+    int tiles;  // of a matrix
+    int full, tail, parts;
+};
+
+struct NsStep {
+    int src;           // which of the two X^T is this step's
+    bool fine, last;   // of the last two steps, the last one
+    bool wide;         // 16-byte stores to the output are aligned
+};
 
 // Tile `tile` of the lower triangle of T x T tiles: groups of GM rows, in a group column
 // by column.
@@ -187,23 +277,40 @@ __device__ __forceinline__ void ns_triangle(int tile, int T, int GM, int& ti, in
     }
 }
 
-// Where 16-byte chunk c of row `row` of the staged output tile lies: chunks XOR-ed with
-// the row so that neither 32 rows at one chunk nor every eighth row at one column meet in
-// few banks.
-template <typename S>
-__device__ __forceinline__ int ns_staged(int row, int c)
+template <typename S, int MODE>
+__device__ __forceinline__ void ns_tile(const NsArgs& g, int tile, int& ti, int& tj)
 {
-    return row * S::BN * 2 + ((c ^ ((row ^ (row >> 3)) & (S::BN / 8 - 1))) << 4);
+    const int tn = (g.m + S::BN - 1) / S::BN;
+    if constexpr (MODE == NS_UPDATE) {
+        const int tm = (g.n + S::BM - 1) / S::BM;
+        const int group = tile / (S::GM * tn), within = tile - group * S::GM * tn, gs = min(S::GM, tm - group * S::GM);
+        ti = group * S::GM + within % gs;
+        tj = within / gs;
+    } else {
+        ns_triangle(tile, tn, S::GM, ti, tj);
+    }
+}
+
+// Where 16-byte chunk c of row `row` of a staged tile lies: chunks XOR-ed with the row so
+// that neither 32 rows at one chunk nor every eighth row at one column meet in few banks.
+template <typename S>
+__device__ __forceinline__ int ns_staged_chunk(int row, int c)
+{
+    return c ^ ((row ^ (row >> 3)) & (S::BN / 8 - 1));
+}
+template <typename S>
+__device__ __forceinline__ int ns_staged(int row, int col)
+{
+    return row * S::BN * 2 + (ns_staged_chunk<S>(row, col / 8) << 4) + col % 8 * 2;
 }
 
 // 8 values to row `row`, columns col .. col + 7 of a matrix of `rows` rows of `cols`
-// values, `pitch` apart: what lies inside.
-__device__ __forceinline__ void ns_put(uint16_t* dst, const uint4& v, int row, int col, int rows, int cols,
-                                       size_t pitch, bool wide)
+// values: what lies inside.
+__device__ __forceinline__ void ns_put(uint16_t* dst, const uint4& v, int row, int col, int rows, int cols, bool wide)
 {
     if (row >= rows || col >= cols)
         return;
-    uint16_t* at = dst + (size_t)row * pitch + col;
+    uint16_t* at = dst + (size_t)row * cols + col;
     if (wide && col + 8 <= cols) {
         *reinterpret_cast<uint4*>(at) = v;
         return;
@@ -215,67 +322,240 @@ __device__ __forceinline__ void ns_put(uint16_t* dst, const uint4& v, int row, i
             at[q] = (uint16_t)(w[q / 2] >> (16 * (q % 2)));
 }
 
-// The staged tile to rows i0 .., columns j0 .. of dst (direct) or, transposed, to rows
-// j0 .., columns i0 ...
-template <typename S, bool TRANSPOSED>
-__device__ __forceinline__ void ns_write(const uint8_t* lds, uint16_t* dst, int i0, int j0, int rows, int cols,
-                                         size_t pitch, bool wide)
+// The tile row of row sr of a staged band: all of a tile's rows are staged, or (ONE)
+// those of row fragment f of every wavefront.
+template <typename S, bool ONE>
+__device__ __forceinline__ int ns_tile_row(int sr, int f)
 {
-    constexpr int kChunks = (TRANSPOSED ? S::BM : S::BN) / 8, kRows = TRANSPOSED ? S::BN : S::BM;
+    return ONE ? sr / 32 * S::kWaveM + f * 32 + sr % 32 : sr;
+}
+
+// The staged rows to rows i0 .., columns j0 .. of dst.
+template <typename S, bool ONE>
+__device__ __forceinline__ void ns_write(const uint8_t* lds, uint16_t* dst, int f, int i0, int j0, int rows, int cols,
+                                         bool wide)
+{
+    constexpr int kChunks = S::BN / 8, kRows = ONE ? S::WM * 32 : S::BM;
+#pragma unroll 4
     for (int it = threadIdx.x; it < kRows * kChunks; it += S::kThreads) {
         const int r = it / kChunks, c = it % kChunks;
-        uint4 v;
-        if constexpr (TRANSPOSED) {
-            uint32_t e[8];
+        const uint4 v = *reinterpret_cast<const uint4*>(lds + ns_staged<S>(r, 8 * c));
+        ns_put(dst, v, i0 + ns_tile_row<S, ONE>(r, f), j0 + 8 * c, rows, cols, wide);
+    }
+}
+
+// The staged rows, transposed, to rows j0 .., columns i0 .. of dst: a thread takes 8 rows
+// of 4 columns.
+template <typename S, bool ONE>
+__device__ __forceinline__ void ns_write_transposed(const uint8_t* lds, uint16_t* dst, int f, int i0, int j0, int rows,
+                                                    int cols, bool wide)
+{
+    constexpr int kChunks = (ONE ? S::WM * 32 : S::BM) / 8;
+#pragma unroll 2
+    for (int it = threadIdx.x; it < S::BN / 4 * kChunks; it += S::kThreads) {
+        const int r = 8 * (it % kChunks), c = 4 * (it / kChunks);
+        uint2 e[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                e[q] = *reinterpret_cast<const uint16_t*>(lds + ns_staged<S>(8 * c + q, r / 8) + (r % 8) * 2);
-            v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-            ns_put(dst, v, j0 + r, i0 + 8 * c, rows, cols, pitch, wide);
-        } else {
-            v = *reinterpret_cast<const uint4*>(lds + ns_staged<S>(r, c));
-            ns_put(dst, v, i0 + r, j0 + 8 * c, rows, cols, pitch, wide);
+        for (int q = 0; q < 8; ++q)
+            e[q] = *reinterpret_cast<const uint2*>(lds + ns_staged<S>(r + q, c));
+        const int col = i0 + ns_tile_row<S, ONE>(r, f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                w[p] = __builtin_amdgcn_perm(q < 2 ? e[2 * p + 1].x : e[2 * p + 1].y, q < 2 ? e[2 * p].x : e[2 * p].y,
+                                             q % 2 ? 0x07060302u : 0x05040100u);
+            ns_put(dst, make_uint4(w[0], w[1], w[2], w[3]), j0 + c + q, col, rows, cols, wide);
         }
     }
 }
 
-// One output tile of a product per block:
-//   GRAM    A = X X^T      POLY    B = b A + c A^2      UPDATE    X^T <- a X^T + X^T B
-// A and B are symmetric: only tiles on and below the diagonal are computed, and stored
-// on both sides of it.
+// What the epilogue needs of a row-major operand at the output tile's place (A of POLY, X^T
+// of UPDATE), into LDS in the staged order; it is replaced there by the output.
+template <typename S, bool ONE>
+__device__ __forceinline__ void ns_fetch(uint8_t* lds, const _Float16* src, int f, int i0, int j0, int rows, int cols)
+{
+    constexpr int kRows = ONE ? S::WM * 32 : S::BM, kChunks = S::BN / 8, kLoadRows = 64 / kChunks;
+    static_assert(kRows % (kLoadRows * S::kWaves) == 0, "loads split evenly");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+    const i32x4 rs = make_rsrc(src + (size_t)i0 * cols, (uint32_t)min(S::BM, rows - i0) * (uint32_t)cols * 2);
+#pragma unroll
+    for (int p = 0; p < kRows / (kLoadRows * S::kWaves); ++p) {
+        const int first = (p * S::kWaves + wave) * kLoadRows, sr = first + lane / kChunks;
+        const int r = ns_tile_row<S, ONE>(sr, f), c = j0 + 8 * ns_staged_chunk<S>(sr, lane % kChunks);
+        const uint32_t voff = i0 + r < rows && c < cols ? ((uint32_t)r * (uint32_t)cols + c) * 2 : 0xf0000000u;
+        dma16(rs, lds_addr(lds) + first * S::BN * 2, voff, 0);
+    }
+}
+
+// Epilogue of the row fragments f0 .. f0 + N - 1 of every wavefront, whose sums are acc
+// [0 .. N): the values that the next product reads.  `lds` is free.
+template <typename S, int MODE, int N>
+__device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size_t mat, int ti, int tj, int f0,
+                                         const f32x16 (&acc)[N][S::kFN], uint8_t* lds)
+{
+    constexpr bool ONE = N != S::kFM;
+    const int i0 = ti * S::BM, j0 = tj * S::BN;
+    int tid = threadIdx.x;
+    __asm__ volatile("" : "+v"(tid));
+    const int lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    if constexpr (MODE == NS_POLY)
+        ns_fetch<S, ONE>(lds, g.a + mat * g.m * g.mp, f0, i0, j0, g.m, g.mp);
+    if constexpr (MODE == NS_UPDATE)
+        ns_fetch<S, ONE>(lds, g.xt + ((size_t)st.src * g.count + mat) * g.n * g.mp, f0, i0, j0, g.n, g.mp);
+    // what the columns of this lane need: the diagonal of A or B there
+    f32x4 dj[S::kFN][4];
+    if constexpr (MODE != NS_GRAM) {
+        const float* d = (MODE == NS_POLY ? g.da : g.db) + mat * g.mp;
+#pragma unroll
+        for (int fj = 0; fj < S::kFN; ++fj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = j0 + (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32 + 8 * q + 4 * (lane >> 5);
+                dj[fj][q] = *reinterpret_cast<const f32x4*>(d + min(j, g.mp - 4));
+            }
+    }
+    const float inv = 1.0f / g.sx;  // powers of two
+    bool ready = false;
+#pragma unroll
+    for (int fi = 0; fi < N; ++fi) {
+        const int sr = ONE ? wm * 32 + (lane & 31) : wm * S::kWaveM + fi * 32 + (lane & 31);
+        const int ib = i0 + wm * S::kWaveM + (f0 + fi) * 32, i = ib + (lane & 31);
+        const bool held_i = ib < (MODE == NS_UPDATE ? g.np : g.mp);
+        // a fragment row's loads leave together: a store in between would hold them back
+        f16x4 low[S::kFN][4];
+        float di = 0.0f;
+        if constexpr (MODE == NS_POLY)
+            di = g.da[mat * g.mp + min(i, g.mp - 1)];
+        if constexpr (MODE == NS_UPDATE)
+#pragma unroll
+            for (int fj = 0; fj < S::kFN; ++fj) {
+                const int jb = j0 + (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    low[fj][q] = held_i && jb < g.mp ? *reinterpret_cast<const f16x4*>(
+                                                           g.low + ns_frag(g, mat, ib / 32, jb / 32) + q * 256 + lane * 4)
+                                                     : f16x4{0, 0, 0, 0};
+            }
+        if (!ready) {  // the fetched tile has to be there
+            wait_vmcnt<0>();
+            lds_barrier();
+            ready = true;
+        }
+#pragma unroll
+        for (int fj = 0; fj < S::kFN; ++fj) {
+            const int c0 = (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32;
+            if (!held_i || j0 + c0 >= g.mp)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = c0 + 8 * q + 4 * (lane >> 5), j = j0 + c;
+                const f32x4 v = {acc[fi][fj][4 * q], acc[fi][fj][4 * q + 1], acc[fi][fj][4 * q + 2],
+                                 acc[fi][fj][4 * q + 3]};
+                f16x4* at = reinterpret_cast<f16x4*>(lds + ns_staged<S>(sr, c));
+                f16x4 o;
+                if constexpr (MODE == NS_GRAM) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float s = v[e] * (inv * inv);
+                        if (j + e == i && i < g.m)
+                            g.da[mat * g.mp + i] = s;
+                        o[e] = (_Float16)(j + e == i ? 0.0f : s * kNsScale);
+                    }
+                } else if constexpr (MODE == NS_POLY) {
+                    const f16x4 a = *at;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float off = (float)a[e] * (1.0f / kNsScale);
+                        const float sq = v[e] * (1.0f / (kNsScale * kNsScale));
+                        if (j + e == i && i < g.m)
+                            g.db[mat * g.mp + i] = fmaf(kNsC, fmaf(di, di, sq), kNsB * di);
+                        const float b = fmaf(kNsC, fmaf(di + dj[fj][q][e], off, sq), kNsB * off);
+                        o[e] = (_Float16)(j + e == i ? 0.0f : b * kNsScale);
+                    }
+                } else {
+                    const f16x4 hi = *at;
+                    f32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float h = (float)hi[e], x = fmaf((float)low[fj][q][e], 1.0f / kNsLow, h);
+                        y[e] = fmaf(kNsA, x, fmaf(dj[fj][q][e], st.fine ? x : h, v[e] * (1.0f / kNsScale)));
+                    }
+                    if (st.last) {
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                        o = __builtin_bit_cast(f16x4, __builtin_convertvector(y * inv, bf16x4));
+                    } else {
+                        f16x4 l;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[e] = (_Float16)y[e];
+                            l[e] = (_Float16)((y[e] - (float)o[e]) * kNsLow);
+                        }
+                        *reinterpret_cast<f16x4*>(g.low + ns_frag(g, mat, ib / 32, (j0 + c0) / 32) + q * 256 + lane * 4) = l;
+                    }
+                }
+                *at = o;
+            }
+        }
+    }
+    lds_barrier();
+    if constexpr (MODE != NS_UPDATE) {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(MODE == NS_GRAM ? g.a : g.b) + mat * g.m * g.mp;
+        ns_write<S, ONE>(lds, dst, f0, i0, j0, g.m, g.mp, true);
+        if (ti != tj)
+            ns_write_transposed<S, ONE>(lds, dst, f0, i0, j0, g.m, g.mp, true);
+    } else if (st.last) {
+        uint16_t* dst = g.out + mat * g.rows * g.cols;
+        if (g.rows > g.cols)
+            ns_write<S, ONE>(lds, dst, f0, i0, j0, g.n, g.m, st.wide);
+        else
+            ns_write_transposed<S, ONE>(lds, dst, f0, i0, j0, g.m, g.n, st.wide);
+    } else {
+        uint16_t* xt = reinterpret_cast<uint16_t*>(g.xt) + ((size_t)(st.src ^ 1) * g.count + mat) * g.n * g.mp;
+        ns_write<S, ONE>(lds, xt, f0, i0, j0, g.n, g.mp, true);
+        ns_write_transposed<S, ONE>(lds, reinterpret_cast<uint16_t*>(g.x) + mat * g.m * g.np, f0, i0, j0, g.m, g.np,
+                                    true);
+    }
+}
+
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd)))
-void moe_ns_product_kernel(NsArgs g, int tiles, int src, bool fine, bool last, bool wide)
+void moe_ns_product_kernel(NsArgs g, NsPlan plan, NsStep st)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     static_assert(S::BM * S::BN * 2 <= S::S * S::kStage, "the staged output tile fits the stages");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
-    // an XCD's blocks take neighbouring tiles
-    const int total = tiles * g.count, each = (total + 7) / 8;
-    const int item = blockIdx.x % 8 * each + blockIdx.x / 8;
-    if (item >= total)
-        return;
-    const size_t mat = item / tiles;
-    const int tile = item % tiles;
-    const int M = MODE == NS_UPDATE ? g.n : g.m, pitch = 2 * (MODE == NS_GRAM ? g.np : g.mp);
-    int ti, tj;
-    if constexpr (MODE == NS_UPDATE) {
-        const int tn = (g.m + S::BN - 1) / S::BN, tm = (g.n + S::BM - 1) / S::BM;
-        const int group = tile / (S::GM * tn), within = tile - group * S::GM * tn, gs = min(S::GM, tm - group * S::GM);
-        ti = group * S::GM + within % gs;
-        tj = within / gs;
+    const int M = MODE == NS_UPDATE ? g.n : g.m, pitch = 2 * (MODE == NS_GRAM ? g.np : g.mp), nk = pitch / S::RB;
+    // an XCD's blocks take neighbouring tiles; the parts of split ones come last
+    int item = blockIdx.x, k0 = 0, k1 = nk, slot = -1;
+    if (item < (plan.full + 7) / 8 * 8) {
+        item = item % 8 * ((plan.full + 7) / 8) + item / 8;
+        if (item >= plan.full)
+            return;
     } else {
-        ns_triangle(tile, (g.m + S::BN - 1) / S::BN, S::GM, ti, tj);
+        item -= (plan.full + 7) / 8 * 8;
+        const int part = item / plan.tail;
+        if (part >= plan.parts)
+            return;
+        item %= plan.tail;
+        slot = item * plan.parts + part;
+        item += plan.full;
+        k0 = part * nk / plan.parts;
+        k1 = (part + 1) * nk / plan.parts;
     }
+    const size_t mat = item / plan.tiles;
+    int ti, tj;
+    ns_tile<S, MODE>(g, item % plan.tiles, ti, tj);
     const int i0 = ti * S::BM, j0 = tj * S::BN;
     const _Float16* A = MODE == NS_GRAM ? g.x + mat * g.m * g.np
                         : MODE == NS_POLY ? g.a + mat * g.m * g.mp
-                                          : g.xt + ((size_t)src * g.count + mat) * g.n * g.mp;
+                                          : g.xt + ((size_t)st.src * g.count + mat) * g.n * g.mp;
     const _Float16* W = MODE == NS_UPDATE ? g.b + mat * g.m * g.mp : A;
 
-    int tid = threadIdx.x;
     const int lane = lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / S::WN, wn = wave % S::WN;
     const uint32_t lds0 = lds_addr(lds);
     const int rowsA = min(S::BM, M - i0), rowsW = min(S::BN, g.m - j0);
@@ -295,8 +575,8 @@ void moe_ns_product_kernel(NsArgs g, int tiles, int src, bool fine, bool last, b
         const int r = lrow + S::kRows * S::kWaves * i;
         voffW[i] = r < rowsW ? (uint32_t)r * (uint32_t)pitch + lchunk : 0xf0000000u;
     }
-    auto issue = [&](int q, int st, int n0, int n1) {
-        const uint32_t dst = lds0 + st * S::kStage + wave * 1024, soff = (uint32_t)q * S::RB;
+    auto issue = [&](int q, int stage, int n0, int n1) {
+        const uint32_t dst = lds0 + stage * S::kStage + wave * 1024, soff = (uint32_t)q * S::RB;
 #pragma unroll
         for (int p = 0; p < S::kLoads; ++p) {
             if (p < n0 || p >= n1)
@@ -309,86 +589,57 @@ void moe_ns_product_kernel(NsArgs g, int tiles, int src, bool fine, bool last, b
     };
     f32x16 acc[S::kFM][S::kFN];
     const int live = min(max((rowsA - wm * S::kWaveM + 31) / 32, 0), S::kFM);
-    tile_product<S, NsOp>(acc, lds, wm, wn, live, 0, pitch / S::RB, issue);
+    tile_product<S, NsOp>(acc, lds, wm, wn, live, k0, k1, issue);
+    if (slot < 0) {
+        ns_store<S, MODE, S::kFM>(g, st, mat, ti, tj, 0, acc, lds);
+        return;
+    }
+    float* dst = g.partial + (size_t)slot * S::kTileFloats;
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(dst + ((((size_t)i * S::kWaves + wave) * S::kFN + j) * 4 + q) * 256 + lane * 4) =
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+#endif
+}
 
-    // Epilogue: the values that the next product reads, staged as 16-bit numbers
-    __asm__ volatile("" : "+v"(tid));
+// The split tiles' parts added in their order, and the epilogue: block (tile, row
+// fragment).
+template <typename S, int MODE>
+__global__ __launch_bounds__(S::kThreads) void moe_ns_tail_kernel(NsArgs g, NsPlan plan, NsStep st)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::WM * 32 * S::BN * 2];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int t = blockIdx.x / S::kFM, f = blockIdx.x % S::kFM, item = plan.full + t;
+    const size_t mat = item / plan.tiles;
+    int ti, tj;
+    ns_tile<S, MODE>(g, item % plan.tiles, ti, tj);
+    // none of the wavefronts' rows is there (those that only pad the transposed output are)
+    if (ti * S::BM + f * 32 >= (MODE == NS_UPDATE ? g.np : g.mp))
+        return;
+    f32x16 acc[1][S::kFN];
 #pragma unroll
-    for (int fi = 0; fi < S::kFM; ++fi)
+    for (int j = 0; j < S::kFN; ++j)
 #pragma unroll
-        for (int fj = 0; fj < S::kFN; ++fj) {
-            const int r = wm * S::kWaveM + fi * 32 + (lane & 31), i = i0 + r;
-            const int c0 = (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32, f0 = j0 + c0;
-            const bool held = f0 < g.mp && i - (lane & 31) < (MODE == NS_UPDATE ? g.np : g.mp);
-            const size_t frag = MODE == NS_UPDATE && held ? ns_frag(g, mat, (i0 + wm * S::kWaveM) / 32 + fi, f0 / 32) : 0;
+        for (int v = 0; v < 16; ++v)
+            acc[0][j][v] = 0.0f;
+    const float* src = g.partial + (size_t)t * plan.parts * S::kTileFloats + (size_t)(f * S::kWaves + wave) * S::kFN * 1024 +
+                       lane * 4;
+    for (int part = 0; part < plan.parts; ++part, src += S::kTileFloats)
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int c = c0 + 8 * q + 4 * (lane >> 5), j = j0 + c;
-                f32x4 v = {acc[fi][fj][4 * q], acc[fi][fj][4 * q + 1], acc[fi][fj][4 * q + 2], acc[fi][fj][4 * q + 3]};
-                f16x4 o = {0, 0, 0, 0};
-                if constexpr (MODE == NS_GRAM) {
-                    const f32x4 s = v * (1.0f / (g.sx * g.sx));
+                const f32x4 p = *reinterpret_cast<const f32x4*>(src + (j * 4 + q) * 256);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (j + e == i && i < g.m)
-                            g.da[mat * g.mp + i] = s[e];
-                        o[e] = (_Float16)(j + e == i ? 0.0f : s[e] * kNsScale);
-                    }
-                } else if constexpr (MODE == NS_POLY) {
-                    if (held && i < g.m) {
-                        const float di = g.da[mat * g.mp + i];
-                        const f32x4 dj = *reinterpret_cast<const f32x4*>(g.da + mat * g.mp + j);
-                        const f16x4 a = *reinterpret_cast<const f16x4*>(g.a + (mat * g.m + i) * g.mp + j);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float off = (float)a[e] * (1.0f / kNsScale);
-                            const float sq = v[e] * (1.0f / (kNsScale * kNsScale));
-                            if (j + e == i)
-                                g.db[mat * g.mp + i] = fmaf(kNsC, fmaf(di, di, sq), kNsB * di);
-                            const float b = fmaf(kNsC, fmaf(di + dj[e], off, sq), kNsB * off);
-                            o[e] = (_Float16)(j + e == i ? 0.0f : b * kNsScale);
-                        }
-                    }
-                } else if (held) {
-                    float* at = g.x32 + frag + q * 256 + lane * 4;
-                    const f32x4 x = *reinterpret_cast<const f32x4*>(at);
-                    const f32x4 db = *reinterpret_cast<const f32x4*>(g.db + mat * g.mp + j);
-                    f32x4 y;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float xr = fine ? x[e] : (float)(_Float16)(x[e] * g.sx) * (1.0f / g.sx);
-                        y[e] = fmaf(kNsA, x[e], fmaf(db[e], xr, v[e] * (1.0f / (kNsScale * g.sx))));
-                    }
-                    if (last) {
-                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                        o = __builtin_bit_cast(f16x4, __builtin_convertvector(y, bf16x4));
-                    } else {
-                        *reinterpret_cast<f32x4*>(at) = y;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = (_Float16)(y[e] * g.sx);
-                    }
-                }
-                *reinterpret_cast<f16x4*>(lds + ns_staged<S>(r, c / 8) + (c % 8) * 2) = o;
+                for (int e = 0; e < 4; ++e)
+                    acc[0][j][4 * q + e] += p[e];
             }
-        }
-    __syncthreads();
-    if constexpr (MODE != NS_UPDATE) {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(MODE == NS_GRAM ? g.a : g.b) + mat * g.m * g.mp;
-        ns_write<S, false>(lds, dst, i0, j0, g.m, g.mp, g.mp, true);
-        if (ti != tj)
-            ns_write<S, true>(lds, dst, i0, j0, g.m, g.mp, g.mp, true);
-    } else if (last) {
-        uint16_t* dst = g.out + mat * g.rows * g.cols;
-        if (g.rows > g.cols)
-            ns_write<S, false>(lds, dst, i0, j0, g.n, g.m, g.m, wide);
-        else
-            ns_write<S, true>(lds, dst, i0, j0, g.m, g.n, g.n, wide);
-    } else {
-        uint16_t* xt = reinterpret_cast<uint16_t*>(g.xt) + ((size_t)(src ^ 1) * g.count + mat) * g.n * g.mp;
-        ns_write<S, false>(lds, xt, i0, j0, g.n, g.mp, g.mp, true);
-        ns_write<S, true>(lds, reinterpret_cast<uint16_t*>(g.x) + mat * g.m * g.np, i0, j0, g.m, g.np, g.np, true);
-    }
+    ns_store<S, MODE, 1>(g, st, mat, ti, tj, f, acc, lds);
 #endif
 }
 
@@ -397,7 +648,41 @@ void moe_ns_product_kernel(NsArgs g, int tiles, int src, bool fine, bool last, b
 namespace {
 using namespace moe;
 
+constexpr int kNsCus = 256;      // of gfx950
+constexpr int kNsMaxParts = 16;  // K parts of a split tile
+constexpr int kNsMinPart = 4;    // slices of a part
+
 size_t ns_round(size_t v) { return (v + 255) / 256 * 256; }
+
+// Whole rounds of tiles in one piece, the rest split where K is long enough.
+template <typename S>
+NsPlan ns_plan(const NsArgs& g, int mode)
+{
+    const long long tn = (g.m + S::BN - 1) / S::BN, tm = (g.n + S::BM - 1) / S::BM;
+    NsPlan p;
+    p.tiles = (int)(mode == NS_UPDATE ? tm * tn : tn * (tn + 1) / 2);
+    const int total = p.tiles * g.count, slots = kNsCus * S::kPerCu, nk = (mode == NS_GRAM ? g.np : g.mp) / 64;
+    p.tail = total % slots;
+    p.parts = p.tail ? std::min(std::min(kNsMaxParts, slots / p.tail), nk / kNsMinPart) : 1;
+    if (p.parts <= 1)
+        p.tail = 0, p.parts = 1;
+    p.full = total - p.tail;
+    return p;
+}
+
+// Whether a product takes the 256 x 256 tiles.
+bool ns_large(const NsArgs& g, int mode)
+{
+    const NsPlan p = ns_plan<NsLarge>(g, mode);
+    return p.full + p.tail * p.parts >= kNsCus * 3 / 4;
+}
+
+template <typename S>
+size_t ns_partial(const NsArgs& g, int mode)
+{
+    const NsPlan p = ns_plan<S>(g, mode);
+    return (size_t)p.tail * (p.parts > 1 ? p.parts : 0) * S::kTileFloats * 4;
+}
 
 // The workspace's pieces; returns its size.
 size_t ns_layout(NsArgs& g, char* ws)
@@ -411,12 +696,16 @@ size_t ns_layout(NsArgs& g, char* ws)
     const size_t c = g.count, cells = c * g.n * g.mp, square = c * g.m * g.mp;
     g.x = (_Float16*)take(2 * c * g.m * g.np);
     g.xt = (_Float16*)take(4 * cells);
-    g.x32 = (float*)take(4 * c * g.np * g.mp);
+    g.low = (_Float16*)take(2 * c * g.np * g.mp);
     g.a = (_Float16*)take(2 * square);
     g.b = (_Float16*)take(2 * square);
     g.da = (float*)take(4 * c * g.mp);
     g.db = (float*)take(4 * c * g.mp);
     g.sums = (double*)take(8 * c * kNsSums);
+    size_t partial = 0;
+    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE})
+        partial = std::max(partial, ns_large(g, mode) ? ns_partial<NsLarge>(g, mode) : ns_partial<NsSmall>(g, mode));
+    g.partial = (float*)take(partial);
     return off;
 }
 
@@ -435,22 +724,20 @@ NsArgs ns_args(int count, int rows, int cols)
     return g;
 }
 
-template <typename S>
-hipError_t launch_steps(const NsArgs& g, int steps, hipStream_t stream)
+template <typename S, int MODE>
+void launch_shape(const NsArgs& g, const NsStep& st, hipStream_t stream)
 {
-    const long long tm = (g.m + S::BN - 1) / S::BN, tn = (g.n + S::BM - 1) / S::BM;
-    const int square = (int)(tm * (tm + 1) / 2), update = (int)(tm * tn);
-    // rows of the output that 16-byte stores fit
-    const bool wide = g.cols % 8 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
-    auto grid = [&](int tiles) { return dim3((unsigned)(((long long)tiles * g.count + 7) / 8 * 8)); };
-    const dim3 block(S::kThreads);
-    for (int s = 0; s < steps; ++s) {
-        const bool fine = s >= steps - 2, last = s == steps - 1;
-        moe_ns_product_kernel<S, NS_GRAM><<<grid(square), block, 0, stream>>>(g, square, s & 1, fine, last, wide);
-        moe_ns_product_kernel<S, NS_POLY><<<grid(square), block, 0, stream>>>(g, square, s & 1, fine, last, wide);
-        moe_ns_product_kernel<S, NS_UPDATE><<<grid(update), block, 0, stream>>>(g, update, s & 1, fine, last, wide);
-    }
-    return hipGetLastError();
+    const NsPlan p = ns_plan<S>(g, MODE);
+    const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + p.tail * p.parts)), block(S::kThreads);
+    moe_ns_product_kernel<S, MODE><<<grid, block, 0, stream>>>(g, p, st);
+    if (p.tail)
+        moe_ns_tail_kernel<S, MODE><<<dim3((unsigned)(p.tail * S::kFM)), block, 0, stream>>>(g, p, st);
+}
+
+template <int MODE>
+void launch_product(const NsArgs& g, const NsStep& st, hipStream_t stream)
+{
+    ns_large(g, MODE) ? launch_shape<NsLarge, MODE>(g, st, stream) : launch_shape<NsSmall, MODE>(g, st, stream);
 }
 }  // namespace
 
@@ -463,14 +750,21 @@ extern "C" size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols)
 // dtype 0 fp32, 1 bf16 gradients [count][rows][cols]; momentum (nullable) fp32; out bf16.
 extern "C" hipError_t moe_launch_orthogonalize(int dtype, const void* grad, float* momentum, float beta, int nesterov,
                                                int count, int rows, int cols, int steps, void* out, void* ws,
-                                               int ncu, hipStream_t stream)
+                                               hipStream_t stream)
 {
     NsArgs g = ns_args(count, rows, cols);
     ns_layout(g, (char*)ws);
     g.grad = grad, g.momentum = momentum, g.out = (uint16_t*)out;
     g.beta = beta, g.src_dtype = dtype, g.nesterov = nesterov;
+    auto aligned = [](const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; };
+    g.vec = cols % 4 == 0 && aligned(grad, dtype == 0 ? 16 : 8) && aligned(momentum, 16);
     moe_ns_sums_kernel<<<dim3(g.parts, count), dim3(256), 0, stream>>>(g);
-    moe_ns_init_kernel<<<dim3(g.mp / 32 * (g.np / 32), count), dim3(256), 0, stream>>>(g);
-    const long long large = (long long)count * ((g.m + 255) / 256) * ((g.n + 255) / 256);
-    return large >= ncu ? launch_steps<NsLarge>(g, steps, stream) : launch_steps<NsSmall>(g, steps, stream);
+    moe_ns_init_kernel<<<dim3(g.mp / 64 * (g.np / 64), count), dim3(256), 0, stream>>>(g);
+    for (int s = 0; s < steps; ++s) {
+        const NsStep st = {s & 1, s >= steps - 2, s == steps - 1, cols % 8 == 0 && aligned(out, 16)};
+        launch_product<NS_GRAM>(g, st, stream);
+        launch_product<NS_POLY>(g, st, stream);
+        launch_product<NS_UPDATE>(g, st, stream);
+    }
+    return hipGetLastError();
 }
