@@ -643,6 +643,225 @@ __global__ __launch_bounds__(S::kThreads) void moe_ns_tail_kernel(NsArgs g, NsPl
 #endif
 }
 
+// ---------------------------------------------------------------- few rows
+// Up to 64 rows the m x m side is small enough for 64 bits and for one workgroup.  Every
+// iterate is a polynomial in A_0 = X X^T times X, and A_k goes along without X:
+//   Q = a + b A + c A^2,   P <- Q P,   A <- Q A Q       (all commute, all symmetric)
+// so the gradient is read twice (A_0, then P X) and the steps in between touch nothing
+// else: three launches in place of 2 + 3 or more a step.  P grows to 3.44^steps where a
+// singular value is close to zero, and an error of A_0 with it: A_0 and P are held in fp64
+// (fp64 matrix cores; A_0's products of fp32 numbers are exact), and P X is an fp32
+// product.
+constexpr int kFewRows = 64;
+constexpr int kSlab = 64;         // columns of X at a time
+constexpr int kSlabPitch = 68;    // of a slab in LDS, [column][row]: neither operand order meets in few banks
+constexpr int kFewBytes = 1 << 20;  // partial sums of A_0 that one workgroup adds, at most
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+struct NsFew {
+    double* partial;  // [count][chunks][mt (mt + 1) / 2][256] partial A_0, tiles on and below the diagonal
+    float* p;         // [count][64][64] P
+    double* inv;      // [count] 1 / |U|
+    int mt, chunks;   // 16-row tiles, workgroups a matrix in the first pass
+};
+
+// Columns k0 .. k0 + 63 of U into LDS; with the momentum's step where FIRST.
+template <bool FIRST>
+__device__ __forceinline__ void ns_load_slab(const NsArgs& g, size_t base, int k0, double scale, float* slab)
+{
+    const bool tall = g.rows > g.cols;
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int r = (tall ? k0 : 0) + tid / 16 + 16 * s, c = (tall ? 0 : k0) + tid % 16 * 4;
+        f32x4 u = {0, 0, 0, 0};
+        if (r < g.rows && c < g.cols) {
+            const size_t at = base + (size_t)r * g.cols + c;
+            const int held = min(4, g.cols - c);
+            if constexpr (FIRST) {
+                u = ns_load_grad(g, at, held);
+                if (g.momentum) {
+                    f32x4 m = ns_load_momentum(g, at, held);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        m[q] = fmaf(g.beta, m[q], u[q]);
+                        u[q] = g.nesterov ? fmaf(g.beta, m[q], u[q]) : m[q];
+                    }
+                    if (g.vec && held == 4)
+                        *reinterpret_cast<f32x4*>(g.momentum + at) = m;
+                    else
+                        for (int q = 0; q < held; ++q)
+                            g.momentum[at + q] = m[q];
+                }
+            } else {
+                u = ns_load_update(g, at, held);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    u[q] = (float)(u[q] * scale);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int k = tall ? tid / 16 + 16 * s : tid % 16 * 4 + q, i = tall ? tid % 16 * 4 + q : tid / 16 + 16 * s;
+            slab[k * kSlabPitch + i] = u[q];
+        }
+    }
+}
+
+// Momentum and partial A_0: block (chunk of the columns, matrix).
+__global__ __launch_bounds__(256) void moe_ns_few_gram_kernel(NsArgs g, NsFew w)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ float slab[kSlab * kSlabPitch];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const size_t mat = blockIdx.y, base = mat * g.rows * g.cols;
+    const int tiles = w.mt * (w.mt + 1) / 2;
+    f64x4 acc[3] = {};  // tiles wave, wave + 4, wave + 8
+    for (int k0 = blockIdx.x * kSlab; k0 < g.n; k0 += w.chunks * kSlab) {
+        __syncthreads();
+        ns_load_slab<true>(g, base, k0, 1.0, slab);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const int t = wave + 4 * q;
+            if (t >= tiles)
+                continue;
+            const int ti = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, tj = t - ti * (ti + 1) / 2;
+            const float* a = slab + (lane / 16) * kSlabPitch + ti * 16 + lane % 16;
+            const float* b = slab + (lane / 16) * kSlabPitch + tj * 16 + lane % 16;
+#pragma unroll 8
+            for (int k = 0; k < kSlab; k += 4)
+                acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[k * kSlabPitch], b[k * kSlabPitch], acc[q], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        if (wave + 4 * q < tiles)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                w.partial[((mat * w.chunks + blockIdx.x) * tiles + wave + 4 * q) * 256 + v * 64 + lane] = acc[q][v];
+#endif
+}
+
+// Element (i, j) of a 16 x 16 tile in the order of the fp64 matrix cores' accumulators.
+__device__ __forceinline__ int ns_f64_at(int i, int j) { return i % 4 * 16 + i / 4 * 64 + j; }
+
+// The steps on A_0 in one workgroup per matrix, a wavefront per 16 x 16 tile.
+__global__ __launch_bounds__(1024) void moe_ns_few_steps_kernel(NsArgs g, NsFew w, int steps)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ double A[kFewRows][kFewRows], P[kFewRows][kFewRows], Q[kFewRows][kFewRows], T[kFewRows][kFewRows];
+    const int lane = lane_id(), wave = threadIdx.x / kWave, M = 16 * w.mt, tiles = w.mt * (w.mt + 1) / 2;
+    const size_t mat = blockIdx.x;
+    const int ti = wave / w.mt, tj = wave % w.mt;
+    const int j = tj * 16 + lane % 16;
+    // this lane's 4 elements of the tile: rows ti * 16 + 4 v + lane / 16, column j
+    const double* src = w.partial + mat * w.chunks * tiles * 256;
+    double sum[4] = {0, 0, 0, 0};
+    const int hi = max(ti, tj), lo = min(ti, tj), tile = hi * (hi + 1) / 2 + lo;
+#pragma unroll 4
+    for (int c = 0; c < w.chunks; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int r = 4 * v + lane / 16, q = lane % 16;
+            sum[v] += src[((size_t)c * tiles + tile) * 256 + (ti >= tj ? ns_f64_at(r, q) : ns_f64_at(q, r))];
+        }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        A[ti * 16 + 4 * v + lane / 16][j] = sum[v];
+    __syncthreads();
+    double trace = 0.0;
+    for (int i = 0; i < g.m; ++i)
+        trace += A[i][i];
+    // zeros stay zeros; a NaN or an infinity anywhere makes the matrix NaN
+    const double inv = trace == 0.0 ? 0.0 : trace * 0.0 + 1.0 / trace;
+    if (threadIdx.x == 0)
+        w.inv[mat] = trace == 0.0 ? 0.0 : trace * 0.0 + 1.0 / sqrt(trace);
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        A[ti * 16 + 4 * v + lane / 16][j] = sum[v] * inv;
+    __syncthreads();
+    auto product = [&](const double (&x)[kFewRows][kFewRows], const double (&y)[kFewRows][kFewRows]) {
+        f64x4 acc = {0, 0, 0, 0};
+        for (int k = 0; k < M; k += 4)  // x is symmetric
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + lane / 16][ti * 16 + lane % 16], y[k + lane / 16][j], acc, 0, 0,
+                                                       0);
+        return acc;
+    };
+    auto store = [&](double (&x)[kFewRows][kFewRows], const f64x4& v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[ti * 16 + 4 * q + lane / 16][j] = v[q];
+    };
+    for (int s = 0; s < steps; ++s) {
+        f64x4 q = product(A, A);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int i = ti * 16 + 4 * v + lane / 16;
+            q[v] = (double)kNsC * q[v] + (double)kNsB * A[i][j] + (i == j ? (double)kNsA : 0.0);
+        }
+        store(Q, q);
+        __syncthreads();
+        f64x4 p = q;
+        if (s > 0)
+            p = product(Q, P);
+        if (s + 1 < steps) {
+            store(T, product(Q, A));
+            __syncthreads();
+            const f64x4 a = product(Q, T);
+            store(A, a);  // T and Q are read only, and A no longer
+        } else {
+            __syncthreads();
+        }
+        store(P, p);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int i = ti * 16 + 4 * v + lane / 16;
+        w.p[(mat * kFewRows + i) * kFewRows + j] = (float)P[i][j];
+    }
+#endif
+}
+
+// out = P X: block (chunk of the columns, matrix).
+__global__ __launch_bounds__(256) void moe_ns_few_apply_kernel(NsArgs g, NsFew w)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ float slab[kSlab * kSlabPitch];
+    __shared__ float P[kFewRows * kSlabPitch];
+    const int lane = lane_id(), wave = threadIdx.x / kWave, M = 16 * w.mt;
+    const size_t mat = blockIdx.y, base = mat * g.rows * g.cols;
+    for (int q = threadIdx.x; q < M * M; q += 256)
+        P[q / M * kSlabPitch + q % M] = w.p[(mat * kFewRows + q / M) * kFewRows + q % M];
+    const double inv = w.inv[mat];
+    const bool tall = g.rows > g.cols;
+    for (int k0 = blockIdx.x * kSlab; k0 < g.n; k0 += gridDim.x * kSlab) {
+        __syncthreads();
+        ns_load_slab<false>(g, base, k0, inv, slab);
+        __syncthreads();
+        // wavefront w: columns 16 w .. of the slab, 16 rows at a time
+        for (int t = 0; t < w.mt; ++t) {
+            f32x4 acc = {0, 0, 0, 0};
+            const float* x = slab + (wave * 16 + lane % 16) * kSlabPitch + lane / 16;
+            const float* p = P + (t * 16 + lane % 16) * kSlabPitch + lane / 16;
+            for (int j = 0; j < M; j += 4)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], x[j], acc, 0, 0, 0);
+            const int k = k0 + wave * 16 + lane % 16;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = t * 16 + 4 * (lane / 16) + v;
+                if (i < g.m && k < g.n)
+                    g.out[base + (tall ? (size_t)k * g.cols + i : (size_t)i * g.cols + k)] =
+                        (uint16_t)f32_to_bf16_bits(acc[v]);
+            }
+        }
+    }
+#endif
+}
+
 }  // namespace moe
 
 namespace {
@@ -682,6 +901,40 @@ size_t ns_partial(const NsArgs& g, int mode)
 {
     const NsPlan p = ns_plan<S>(g, mode);
     return (size_t)p.tail * (p.parts > 1 ? p.parts : 0) * S::kTileFloats * 4;
+}
+
+// Workgroups a matrix of the first pass over few rows: enough for every CU, as long as
+// there are columns and the sums of one matrix are not too much for the workgroup that
+// adds them.
+NsFew few_plan(const NsArgs& g)
+{
+    NsFew w = {};
+    w.mt = (g.m + 15) / 16;
+    const int slabs = (g.n + kSlab - 1) / kSlab, most = kFewBytes / (w.mt * (w.mt + 1) / 2 * 256 * 8);
+    w.chunks = std::min(std::min(slabs, most), std::max(1, 2 * kNsCus / g.count));
+    return w;
+}
+
+size_t few_layout(NsFew& w, const NsArgs& g, char* ws)
+{
+    const size_t c = g.count, partial = ns_round(8 * c * w.chunks * (w.mt * (w.mt + 1) / 2) * 256);
+    const size_t p = ns_round(4 * c * kFewRows * kFewRows);
+    w.partial = (double*)ws;
+    w.p = (float*)(ws + partial);
+    w.inv = (double*)(ws + partial + p);
+    return partial + p + ns_round(8 * c);
+}
+
+hipError_t launch_few(const NsArgs& g, int steps, char* ws, hipStream_t stream)
+{
+    NsFew w = few_plan(g);
+    few_layout(w, g, ws);
+    const int slabs = (g.n + kSlab - 1) / kSlab;
+    moe_ns_few_gram_kernel<<<dim3(w.chunks, g.count), dim3(256), 0, stream>>>(g, w);
+    moe_ns_few_steps_kernel<<<dim3(g.count), dim3(64 * w.mt * w.mt), 0, stream>>>(g, w, steps);
+    moe_ns_few_apply_kernel<<<dim3(std::min(slabs, std::max(1, 8 * kNsCus / g.count)), g.count), dim3(256), 0, stream>>>(
+        g, w);
+    return hipGetLastError();
 }
 
 // The workspace's pieces; returns its size.
@@ -744,6 +997,12 @@ void launch_product(const NsArgs& g, const NsStep& st, hipStream_t stream)
 extern "C" size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols)
 {
     NsArgs g = ns_args(count, rows, cols);
+    if (count == 0)
+        return 0;
+    if (g.m <= kFewRows) {
+        NsFew w = few_plan(g);
+        return few_layout(w, g, nullptr);
+    }
     return ns_layout(g, nullptr);
 }
 
@@ -753,11 +1012,13 @@ extern "C" hipError_t moe_launch_orthogonalize(int dtype, const void* grad, floa
                                                hipStream_t stream)
 {
     NsArgs g = ns_args(count, rows, cols);
-    ns_layout(g, (char*)ws);
     g.grad = grad, g.momentum = momentum, g.out = (uint16_t*)out;
     g.beta = beta, g.src_dtype = dtype, g.nesterov = nesterov;
     auto aligned = [](const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; };
     g.vec = cols % 4 == 0 && aligned(grad, dtype == 0 ? 16 : 8) && aligned(momentum, 16);
+    if (g.m <= kFewRows)
+        return launch_few(g, steps, (char*)ws, stream);
+    ns_layout(g, (char*)ws);
     moe_ns_sums_kernel<<<dim3(g.parts, count), dim3(256), 0, stream>>>(g);
     moe_ns_init_kernel<<<dim3(g.mp / 64 * (g.np / 64), count), dim3(256), 0, stream>>>(g);
     for (int s = 0; s < steps; ++s) {

@@ -102,6 +102,26 @@ def test_steps(steps):
         check(out[i], g[i].double().cpu().numpy(), steps)
 
 
+@pytest.mark.parametrize("steps", [1, 2, 5, 9])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (40, 3, 5), (2, 16, 700), (1, 17, 6000), (3, 32, 33), (2, 5000, 33), (300, 48, 49),
+                                   (2, 64, 1111), (1, 64, 64)], ids=lambda s: "-".join(map(str, s)))
+def test_few_rows_keep_fp32(shape, steps):
+    """Up to 64 rows the steps run on fp64 sums and the last product on fp32 numbers:
+    beyond bf16's rounding (0.577 U8 in the root mean square, U8 for one value) an error of
+    (m + 2) U24 of a sum of products of P, whose largest value is 3.44^steps, and X."""
+    g = dev(gradients(gen(sum(shape) + steps), *shape, "full"))
+    out = run(g, steps=steps).double().cpu().numpy()
+    for i in range(0, shape[0], max(1, shape[0] // 5)):
+        u = g[i].double().cpu().numpy()
+        want = ref.orthogonal(u, steps)
+        m = min(shape[1:])
+        size = (m + 2) * ref.U24 * 3.4445 ** min(steps, 5) * np.sqrt(m)
+        d = np.abs(out[i] - want)
+        assert np.all(d <= ref.U8 * np.abs(want) * 1.001 + size), f"matrix {i}: {(d - ref.U8 * np.abs(want)).max():.3e}"
+        if m * max(shape[1:]) >= 256:
+            assert np.linalg.norm(d) <= (0.6 * ref.U8 + 1e-5) * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("shape", [(1, 200, 300), (1, 640, 256)], ids=lambda s: "-".join(map(str, s)))
 def test_low_rank(shape):
     """Three tokens' gradient: three singular values, the others zero, stay so."""

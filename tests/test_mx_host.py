@@ -163,10 +163,17 @@ def test_orthogonalize_refusals(kw, want):
 
 
 def test_orthogonalize_workspace_covers_every_orientation():
-    for count, rows, cols in ((1, 1, 1), (3, 7, 100), (3, 100, 7), (2, 4096, 14336), (1, 1, 65536)):
+    for count, rows, cols in ((3, 65, 100), (3, 100, 65), (2, 4096, 14336), (1, 65, 65536)):
         n = moe.moe_orthogonalize_workspace_size(count, rows, cols)
-        # the fp32 iterate, both fp16 orientations, and the two square products
+        # X in both orientations (one of them twice) and its remainder, and the two square
+        # products, all of them fp16
         assert n >= count * (8 * rows * cols + 4 * min(rows, cols) ** 2)
+        assert n == moe.moe_orthogonalize_workspace_size(count, cols, rows)
+    for count, rows, cols in ((1, 1, 1), (3, 7, 100), (5, 64, 64), (1, 1, 65536), (32768, 8, 16)):
+        n = moe.moe_orthogonalize_workspace_size(count, rows, cols)
+        # up to 64 rows: their products in fp64, summed and in parts, and the polynomial
+        assert n >= count * (8 * min(rows, cols) ** 2 + 4 * 64 * 64)
+        assert n == moe.moe_orthogonalize_workspace_size(count, cols, rows)
 
 
 # ------------------------------------------------- the binding: element types, sizes, devices
