@@ -655,7 +655,7 @@ __global__ __launch_bounds__(S::kThreads) void moe_ns_tail_kernel(NsArgs g, NsPl
 constexpr int kFewRows = 64;
 constexpr int kSlab = 64;         // columns of X at a time
 constexpr int kSlabPitch = 68;    // of a slab in LDS, [column][row]: neither operand order meets in few banks
-constexpr int kFewBytes = 1 << 20;  // partial sums of A_0 that one workgroup adds, at most
+constexpr int kFewBytes = 1 << 19;  // partial sums of A_0 that one workgroup adds, at most
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -709,6 +709,13 @@ __device__ __forceinline__ void ns_load_slab(const NsArgs& g, size_t base, int k
     }
 }
 
+// The tile on or below the diagonal with number t.
+__device__ __forceinline__ void ns_few_tile(int t, int& ti, int& tj)
+{
+    ti = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+    tj = t - ti * (ti + 1) / 2;
+}
+
 // Momentum and partial A_0: block (chunk of the columns, matrix).
 __global__ __launch_bounds__(256) void moe_ns_few_gram_kernel(NsArgs g, NsFew w)
 {
@@ -727,7 +734,8 @@ __global__ __launch_bounds__(256) void moe_ns_few_gram_kernel(NsArgs g, NsFew w)
             const int t = wave + 4 * q;
             if (t >= tiles)
                 continue;
-            const int ti = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, tj = t - ti * (ti + 1) / 2;
+            int ti, tj;
+            ns_few_tile(t, ti, tj);
             const float* a = slab + (lane / 16) * kSlabPitch + ti * 16 + lane % 16;
             const float* b = slab + (lane / 16) * kSlabPitch + tj * 16 + lane % 16;
 #pragma unroll 8
@@ -744,32 +752,34 @@ __global__ __launch_bounds__(256) void moe_ns_few_gram_kernel(NsArgs g, NsFew w)
 #endif
 }
 
-// Element (i, j) of a 16 x 16 tile in the order of the fp64 matrix cores' accumulators.
-__device__ __forceinline__ int ns_f64_at(int i, int j) { return i % 4 * 16 + i / 4 * 64 + j; }
-
-// The steps on A_0 in one workgroup per matrix, a wavefront per 16 x 16 tile.
-__global__ __launch_bounds__(1024) void moe_ns_few_steps_kernel(NsArgs g, NsFew w, int steps)
+// The steps on A_0 in one workgroup per matrix, a wavefront per 16 x 16 tile on or below
+// the diagonal, which it stores on both sides.
+__global__ __launch_bounds__(640) void moe_ns_few_steps_kernel(NsArgs g, NsFew w, int steps)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     __shared__ double A[kFewRows][kFewRows], P[kFewRows][kFewRows], Q[kFewRows][kFewRows], T[kFewRows][kFewRows];
     const int lane = lane_id(), wave = threadIdx.x / kWave, M = 16 * w.mt, tiles = w.mt * (w.mt + 1) / 2;
     const size_t mat = blockIdx.x;
-    const int ti = wave / w.mt, tj = wave % w.mt;
-    const int j = tj * 16 + lane % 16;
-    // this lane's 4 elements of the tile: rows ti * 16 + 4 v + lane / 16, column j
-    const double* src = w.partial + mat * w.chunks * tiles * 256;
-    double sum[4] = {0, 0, 0, 0};
-    const int hi = max(ti, tj), lo = min(ti, tj), tile = hi * (hi + 1) / 2 + lo;
-#pragma unroll 4
+    int ti, tj;
+    ns_few_tile(wave, ti, tj);
+    // this lane's 4 elements of the tile: rows i0 + 4 v, column j
+    const int i0 = ti * 16 + lane / 16, j = tj * 16 + lane % 16;
+    auto store = [&](double (&x)[kFewRows][kFewRows], const f64x4& v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[i0 + 4 * q][j] = v[q];
+            if (ti != tj)
+                x[j][i0 + 4 * q] = v[q];
+        }
+    };
+    const double* src = w.partial + (mat * w.chunks * tiles + wave) * 256 + lane;
+    f64x4 sum = {0, 0, 0, 0};
+#pragma unroll 8
     for (int c = 0; c < w.chunks; ++c)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int r = 4 * v + lane / 16, q = lane % 16;
-            sum[v] += src[((size_t)c * tiles + tile) * 256 + (ti >= tj ? ns_f64_at(r, q) : ns_f64_at(q, r))];
-        }
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-        A[ti * 16 + 4 * v + lane / 16][j] = sum[v];
+        for (int v = 0; v < 4; ++v)
+            sum[v] += src[(size_t)c * tiles * 256 + v * 64];
+    store(A, sum);
     __syncthreads();
     double trace = 0.0;
     for (int i = 0; i < g.m; ++i)
@@ -779,29 +789,21 @@ __global__ __launch_bounds__(1024) void moe_ns_few_steps_kernel(NsArgs g, NsFew 
     if (threadIdx.x == 0)
         w.inv[mat] = trace == 0.0 ? 0.0 : trace * 0.0 + 1.0 / sqrt(trace);
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-        A[ti * 16 + 4 * v + lane / 16][j] = sum[v] * inv;
+    store(A, sum * inv);
     __syncthreads();
     auto product = [&](const double (&x)[kFewRows][kFewRows], const double (&y)[kFewRows][kFewRows]) {
         f64x4 acc = {0, 0, 0, 0};
-        for (int k = 0; k < M; k += 4)  // x is symmetric
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + lane / 16][ti * 16 + lane % 16], y[k + lane / 16][j], acc, 0, 0,
-                                                       0);
-        return acc;
-    };
-    auto store = [&](double (&x)[kFewRows][kFewRows], const f64x4& v) {
+        for (int k = 0; k < M; k += 16)  // x is symmetric
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            x[ti * 16 + 4 * q + lane / 16][j] = v[q];
+            for (int q = lane / 16, n = 0; n < 4; ++n, q += 4)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + q][ti * 16 + lane % 16], y[k + q][j], acc, 0, 0, 0);
+        return acc;
     };
     for (int s = 0; s < steps; ++s) {
         f64x4 q = product(A, A);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int i = ti * 16 + 4 * v + lane / 16;
-            q[v] = (double)kNsC * q[v] + (double)kNsB * A[i][j] + (i == j ? (double)kNsA : 0.0);
-        }
+        for (int v = 0; v < 4; ++v)
+            q[v] = (double)kNsC * q[v] + (double)kNsB * A[i0 + 4 * v][j] + (i0 + 4 * v == j ? (double)kNsA : 0.0);
         store(Q, q);
         __syncthreads();
         f64x4 p = q;
@@ -810,19 +812,15 @@ __global__ __launch_bounds__(1024) void moe_ns_few_steps_kernel(NsArgs g, NsFew 
         if (s + 1 < steps) {
             store(T, product(Q, A));
             __syncthreads();
-            const f64x4 a = product(Q, T);
-            store(A, a);  // T and Q are read only, and A no longer
+            store(A, product(Q, T));  // T and Q are read only, and A no longer
         } else {
             __syncthreads();
         }
         store(P, p);
         __syncthreads();
     }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int i = ti * 16 + 4 * v + lane / 16;
-        w.p[(mat * kFewRows + i) * kFewRows + j] = (float)P[i][j];
-    }
+    for (int q = threadIdx.x; q < M * M; q += blockDim.x)
+        w.p[(mat * kFewRows + q / M) * kFewRows + q % M] = (float)P[q / M][q % M];
 #endif
 }
 
@@ -931,7 +929,7 @@ hipError_t launch_few(const NsArgs& g, int steps, char* ws, hipStream_t stream)
     few_layout(w, g, ws);
     const int slabs = (g.n + kSlab - 1) / kSlab;
     moe_ns_few_gram_kernel<<<dim3(w.chunks, g.count), dim3(256), 0, stream>>>(g, w);
-    moe_ns_few_steps_kernel<<<dim3(g.count), dim3(64 * w.mt * w.mt), 0, stream>>>(g, w, steps);
+    moe_ns_few_steps_kernel<<<dim3(g.count), dim3(64 * (w.mt * (w.mt + 1) / 2)), 0, stream>>>(g, w, steps);
     moe_ns_few_apply_kernel<<<dim3(std::min(slabs, std::max(1, 8 * kNsCus / g.count)), g.count), dim3(256), 0, stream>>>(
         g, w);
     return hipGetLastError();

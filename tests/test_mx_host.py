@@ -171,8 +171,9 @@ def test_orthogonalize_workspace_covers_every_orientation():
         assert n == moe.moe_orthogonalize_workspace_size(count, cols, rows)
     for count, rows, cols in ((1, 1, 1), (3, 7, 100), (5, 64, 64), (1, 1, 65536), (32768, 8, 16)):
         n = moe.moe_orthogonalize_workspace_size(count, rows, cols)
-        # up to 64 rows: their products in fp64, summed and in parts, and the polynomial
-        assert n >= count * (8 * min(rows, cols) ** 2 + 4 * 64 * 64)
+        # up to 64 rows: their products on and below the diagonal in fp64, the polynomial in fp32
+        m = min(rows, cols)
+        assert n >= count * (4 * m * (m + 1) + 4 * m * m)
         assert n == moe.moe_orthogonalize_workspace_size(count, cols, rows)
 
 
