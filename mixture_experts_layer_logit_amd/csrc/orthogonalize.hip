@@ -871,34 +871,49 @@ constexpr int kNsMinPart = 4;    // slices of a part
 
 size_t ns_round(size_t v) { return (v + 255) / 256 * 256; }
 
-// Whole rounds of tiles in one piece, the rest split where K is long enough.
+// A product's plan on tiles of one shape and its time in us, fitted to traces of 512 to
+// 4096 rows, 512 to 14336 columns and 1 to 64 matrices (within a fifth; 128 x 128 tiles
+// two to a CU).  With f the share of the blocks that run at a time:
+//   a slice                        256: 0.95 + 0.75 f      128: 0.43 + 0.57 f
+//   launch, first loads, epilogue  256: 15 (UPDATE 20 + 8 f)  128: 8 (UPDATE 10 + 5 f)
+//   in parts: the tail kernel and the partial tiles' traffic in place of the epilogue
+// Whole rounds of tiles stay in one piece; the rest goes in the number of parts along K
+// that is the fastest.  Measured, 256 x 256 / split, 128 x 128 / split:
+//   A of 1 of 500 x 6000     99 / 29   46 / 22     X of 64 of 1024 x 512   90 / 90   102 / 103
+//   A of 16 of 1024 x 512    28 / 30   15 / 25     X of 16 of 1024 x 512   30 / 52    22 / 24
+//   A of 1 of 2048 x 2048    44 / 40   22 / 25     X of 1 of 4096 x 4096  131 / 131  148 / 148
 template <typename S>
-NsPlan ns_plan(const NsArgs& g, int mode)
+double ns_plan(const NsArgs& g, int mode, NsPlan& p)
 {
+    const bool big = S::BM == 256;
     const long long tn = (g.m + S::BN - 1) / S::BN, tm = (g.n + S::BM - 1) / S::BM;
-    NsPlan p;
     p.tiles = (int)(mode == NS_UPDATE ? tm * tn : tn * (tn + 1) / 2);
     const int total = p.tiles * g.count, slots = kNsCus * S::kPerCu, nk = (mode == NS_GRAM ? g.np : g.mp) / 64;
-    p.tail = total % slots;
-    p.parts = p.tail ? std::min(std::min(kNsMaxParts, slots / p.tail), nk / kNsMinPart) : 1;
-    if (p.parts <= 1)
-        p.tail = 0, p.parts = 1;
+    auto slice = [&](double f) { return big ? 0.95 + 0.75 * f : 0.43 + 0.57 * f; };
+    auto round = [&](double f) {
+        return (mode == NS_UPDATE ? (big ? 20 + 8 * f : 10 + 5 * f) : big ? 15.0 : 8.0) + nk * slice(f);
+    };
+    const int rest = total % slots;
+    double time = total / slots * round(1.0), best = rest ? round((double)rest / slots) : 0.0;
+    p.parts = 1;
+    for (int parts = 2; rest && parts <= std::min(std::min(kNsMaxParts, slots / rest), nk / kNsMinPart); ++parts) {
+        const double blocks = (double)rest * parts, mb = blocks * S::kTileFloats * 4e-6;
+        const double t = (big ? 15.0 : 10.0) + (nk + parts - 1) / parts * slice(blocks / slots) + 0.5 * parts + 0.25 * mb;
+        if (t < best)
+            best = t, p.parts = parts;
+    }
+    p.tail = p.parts > 1 ? rest : 0;
     p.full = total - p.tail;
-    return p;
+    return time + best;
 }
 
-// Whether a product takes the 256 x 256 tiles.
-bool ns_large(const NsArgs& g, int mode)
+// Whether a product takes the 256 x 256 tiles, and its plan.
+bool ns_large(const NsArgs& g, int mode, NsPlan& p)
 {
-    const NsPlan p = ns_plan<NsLarge>(g, mode);
-    return p.full + p.tail * p.parts >= kNsCus * 3 / 4;
-}
-
-template <typename S>
-size_t ns_partial(const NsArgs& g, int mode)
-{
-    const NsPlan p = ns_plan<S>(g, mode);
-    return (size_t)p.tail * (p.parts > 1 ? p.parts : 0) * S::kTileFloats * 4;
+    NsPlan large, small;
+    const bool is = ns_plan<NsLarge>(g, mode, large) <= ns_plan<NsSmall>(g, mode, small);
+    p = is ? large : small;
+    return is;
 }
 
 // Workgroups a matrix of the first pass over few rows: enough for every CU, as long as
@@ -954,8 +969,11 @@ size_t ns_layout(NsArgs& g, char* ws)
     g.db = (float*)take(4 * c * g.mp);
     g.sums = (double*)take(8 * c * kNsSums);
     size_t partial = 0;
-    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE})
-        partial = std::max(partial, ns_large(g, mode) ? ns_partial<NsLarge>(g, mode) : ns_partial<NsSmall>(g, mode));
+    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE}) {
+        NsPlan p;
+        const int floats = ns_large(g, mode, p) ? NsLarge::kTileFloats : NsSmall::kTileFloats;
+        partial = std::max(partial, (size_t)p.tail * p.parts * floats * 4);
+    }
     g.partial = (float*)take(partial);
     return off;
 }
@@ -976,19 +994,24 @@ NsArgs ns_args(int count, int rows, int cols)
 }
 
 template <typename S, int MODE>
-void launch_shape(const NsArgs& g, const NsStep& st, hipStream_t stream)
+void launch_shape(const NsArgs& g, const NsPlan& p, const NsStep& st, hipStream_t stream)
 {
-    const NsPlan p = ns_plan<S>(g, MODE);
     const dim3 grid((unsigned)((p.full + 7) / 8 * 8 + p.tail * p.parts)), block(S::kThreads);
     moe_ns_product_kernel<S, MODE><<<grid, block, 0, stream>>>(g, p, st);
     if (p.tail)
         moe_ns_tail_kernel<S, MODE><<<dim3((unsigned)(p.tail * S::kFM)), block, 0, stream>>>(g, p, st);
 }
 
+// How each of a step's products is run, the same in every step.
+struct NsChoice {
+    bool large;
+    NsPlan plan;
+};
+
 template <int MODE>
-void launch_product(const NsArgs& g, const NsStep& st, hipStream_t stream)
+void launch_product(const NsArgs& g, const NsChoice& c, const NsStep& st, hipStream_t stream)
 {
-    ns_large(g, MODE) ? launch_shape<NsLarge, MODE>(g, st, stream) : launch_shape<NsSmall, MODE>(g, st, stream);
+    c.large ? launch_shape<NsLarge, MODE>(g, c.plan, st, stream) : launch_shape<NsSmall, MODE>(g, c.plan, st, stream);
 }
 }  // namespace
 
@@ -1019,11 +1042,14 @@ extern "C" hipError_t moe_launch_orthogonalize(int dtype, const void* grad, floa
     ns_layout(g, (char*)ws);
     moe_ns_sums_kernel<<<dim3(g.parts, count), dim3(256), 0, stream>>>(g);
     moe_ns_init_kernel<<<dim3(g.mp / 64 * (g.np / 64), count), dim3(256), 0, stream>>>(g);
+    NsChoice c[3];
+    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE})
+        c[mode].large = ns_large(g, mode, c[mode].plan);
     for (int s = 0; s < steps; ++s) {
         const NsStep st = {s & 1, s >= steps - 2, s == steps - 1, cols % 8 == 0 && aligned(out, 16)};
-        launch_product<NS_GRAM>(g, st, stream);
-        launch_product<NS_POLY>(g, st, stream);
-        launch_product<NS_UPDATE>(g, st, stream);
+        launch_product<NS_GRAM>(g, c[NS_GRAM], st, stream);
+        launch_product<NS_POLY>(g, c[NS_POLY], st, stream);
+        launch_product<NS_UPDATE>(g, c[NS_UPDATE], st, stream);
     }
     return hipGetLastError();
 }
