@@ -521,8 +521,6 @@ def _mx_check(codes=(), scales=(), others=()):
     that is no MXFP4 codes, no E8M0 scales or, of others (name, tensor, type, least),
     another type, or that has too few elements: the kernels would read the bytes as
     something else, or go past their end.  None and plain addresses pass."""
-    if not _packed:
-        _fill_packed()
     for name, t, least in codes:
         if t is None or isinstance(t, int):
             continue
@@ -537,60 +535,73 @@ def _mx_check(codes=(), scales=(), others=()):
             raise TypeError(f"{name}: scales are E8M0 (uint8 or float8_e8m0fnu), not {t.dtype}")
         if t.numel() < least:
             raise ValueError(f"{name}: {t.numel()} elements, {least} are needed")
-    if others:
-        _refuse(((n, t, of) for n, t, of, _ in others), ((n, t, least) for n, t, _, least in others))
+    _refuse([(n, t, of) for n, t, of, _ in others], [(n, t, least) for n, t, _, least in others])
 
 
-def _on_gpu(stream, **tensors):
+def _mx_fits(codes, scales):
+    """Whether (tensor, least) pairs are MXFP4 codes and E8M0 scales of at least that
+    size; AttributeError for None and plain addresses."""
+    for t, least in codes:
+        if t.dtype not in _packed or t.numel() < least:
+            return False
+    for t, least in scales:
+        if _scale_types.get(t.dtype) != MOE_SCALE_E8M0 or t.numel() < least:
+            return False
+    return True
+
+
+def _on_gpu(stream, tensors):
     """ValueError for a tensor that is not on the GPU the call runs on: the current
     one, or any single one where a stream is given.  None and plain addresses pass."""
     at = None
-    for name, t in tensors.items():
+    for t in tensors:
         if t is None or isinstance(t, int):
             continue
         here = t.get_device()
-        if here < 0:
-            raise ValueError(f"{name} is not on a GPU")
-        if at is None:
-            if stream is None:
+        if here != at:
+            if here < 0:
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} is not on a GPU")
+            if at is None:
+                at = here
+                if stream is not None:
+                    continue
                 import torch
                 at = torch.cuda.current_device()
-            else:
-                at = here
-        if here != at:
-            raise ValueError(f"{name} is on GPU {here}, not on GPU {at}")
+                if here == at:
+                    continue
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on GPU {here}, not on GPU {at}")
+
+
+def _quantised_rows(wide, name, codes, scales, stream):
+    """Checks of a quantiser's (wide rows, codes, scales); their type, rows and K."""
+    if not _packed:
+        _fill_packed()
+    dt = _src_types.get(wide.dtype)
+    if dt is None:
+        raise TypeError(f"{name} is float32 or bfloat16, not {wide.dtype}")
+    n, K = wide.numel(), wide.shape[-1] if wide.dim() else 1
+    try:
+        fits = _mx_fits(((codes, n // 2),), ((scales, n // 32),))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _mx_check((("codes", codes, n // 2),), (("scales", scales, n // 32),))
+    _on_gpu(stream, (wide, codes, scales))
+    return dt, n // (K or 1), K
 
 
 def moe_quantize_mxfp4(src, codes, scales, stream=None):
     """Rows of src (fp32 or bf16 tensor [rows, K]) to MXFP4: E2M1 codes (uint8 [rows,
     K / 2], two to a byte) and an E8M0 scale per 32 values (uint8 or float8_e8m0fnu
     [rows, K / 32])."""
-    if not _packed:
-        _fill_packed()
-    dt = _src_types.get(src.dtype)
-    if dt is None:
-        raise TypeError(f"src is float32 or bfloat16, not {src.dtype}")
-    n, K = src.numel(), src.shape[-1]
-    if not (codes.dtype in _packed and _scale_types.get(scales.dtype) == MOE_SCALE_E8M0 and codes.numel() >= n // 2
-            and scales.numel() >= n // 32):
-        _mx_check((("codes", codes, n // 2),), (("scales", scales, n // 32),))
-    _on_gpu(stream, src=src, codes=codes, scales=scales)
-    _check(load().moe_quantize_mxfp4(_ptr(src), dt, n // (K or 1), K, _ptr(codes), _ptr(scales), _stream(stream)))
+    dt, rows, K = _quantised_rows(src, "src", codes, scales, stream)
+    _check(load().moe_quantize_mxfp4(_ptr(src), dt, rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
 
 
 def moe_dequantize_mxfp4(codes, scales, dst, stream=None):
     """The values of MXFP4 codes and scales, into dst (fp32 or bf16 [rows, K])."""
-    if not _packed:
-        _fill_packed()
-    dt = _src_types.get(dst.dtype)
-    if dt is None:
-        raise TypeError(f"dst is float32 or bfloat16, not {dst.dtype}")
-    n, K = dst.numel(), dst.shape[-1]
-    if not (codes.dtype in _packed and _scale_types.get(scales.dtype) == MOE_SCALE_E8M0 and codes.numel() >= n // 2
-            and scales.numel() >= n // 32):
-        _mx_check((("codes", codes, n // 2),), (("scales", scales, n // 32),))
-    _on_gpu(stream, codes=codes, scales=scales, dst=dst)
-    _check(load().moe_dequantize_mxfp4(_ptr(codes), _ptr(scales), n // (K or 1), K, _ptr(dst), dt, _stream(stream)))
+    dt, rows, K = _quantised_rows(dst, "dst", codes, scales, stream)
+    _check(load().moe_dequantize_mxfp4(_ptr(codes), _ptr(scales), rows, K, _ptr(dst), dt, _stream(stream)))
 
 
 def moe_mxfp4_workspace_size(p) -> int:
@@ -602,41 +613,75 @@ def moe_mxfp4_workspace_size(p) -> int:
 def moe_expert_up_mxfp4(p, aq, a_scale, src_token, offsets, W1q, w1s, hq, hs, ws=None, stream=None):
     """aq, a_scale: codes and scales of x (rows gathered through src_token) or of the
     permuted rows (src_token None); hq, hs: out."""
+    if not _packed:
+        _fill_packed()
     T, d, E, F, rows = p.T, p.d, p.E, p.F, p.T * p.k
-    n1, a = 2 * F if p.act == MOE_ACT_SWIGLU else F, rows if src_token is None else T
-    _mx_check((("aq", aq, a * d // 2), ("W1q", W1q, E * n1 * d // 2), ("hq", hq, rows * F // 2)),
-              (("a_scale", a_scale, a * d // 32), ("w1s", w1s, E * n1 * d // 32), ("hs", hs, rows * F // 32)),
-              (("src_token", src_token, _i32, rows), ("offsets", offsets, _i32, E + 1)))
-    _on_gpu(stream, aq=aq, a_scale=a_scale, src_token=src_token, offsets=offsets, W1q=W1q, w1s=w1s, hq=hq, hs=hs, ws=ws)
+    n1, a = 2 * F if p.act == MOE_ACT_SWIGLU else F, (rows if src_token is None else T) * d
+    w, h = E * n1 * d, rows * F
+    try:
+        fits = (_mx_fits(((aq, a // 2), (W1q, w // 2), (hq, h // 2)), ((a_scale, a // 32), (w1s, w // 32), (hs, h // 32)))
+                and offsets.dtype is _i32 and offsets.numel() > E
+                and (src_token is None or src_token.dtype is _i32 and src_token.numel() >= rows))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _mx_check((("aq", aq, a // 2), ("W1q", W1q, w // 2), ("hq", hq, h // 2)),
+                  (("a_scale", a_scale, a // 32), ("w1s", w1s, w // 32), ("hs", hs, h // 32)),
+                  (("src_token", src_token, _i32, rows), ("offsets", offsets, _i32, E + 1)))
+    _on_gpu(stream, (aq, a_scale, src_token, offsets, W1q, w1s, hq, hs, ws))
     _check(load().moe_expert_up_mxfp4(ctypes.byref(p), _ptr(aq), _ptr(a_scale), _ptr(src_token), _ptr(offsets),
                                       _ptr(W1q), _ptr(w1s), _ptr(hq), _ptr(hs), _ptr(ws), _nbytes(ws),
                                       _stream(stream)))
 
 
 def moe_expert_down_mxfp4(p, hq, hs, offsets, W2q, w2s, y_perm, ws=None, stream=None):
+    if not _packed:
+        _fill_packed()
     d, E, F, rows = p.d, p.E, p.F, p.T * p.k
-    _mx_check((("hq", hq, rows * F // 2), ("W2q", W2q, E * d * F // 2)),
-              (("hs", hs, rows * F // 32), ("w2s", w2s, E * d * F // 32)),
-              (("offsets", offsets, _i32, E + 1), ("y_perm", y_perm, _bf16, rows * d)))
-    _on_gpu(stream, hq=hq, hs=hs, offsets=offsets, W2q=W2q, w2s=w2s, y_perm=y_perm, ws=ws)
+    w, h = E * d * F, rows * F
+    try:
+        fits = (_mx_fits(((hq, h // 2), (W2q, w // 2)), ((hs, h // 32), (w2s, w // 32)))
+                and offsets.dtype is _i32 and offsets.numel() > E
+                and y_perm.dtype is _bf16 and y_perm.numel() >= rows * d)
+    except AttributeError:
+        fits = False
+    if not fits:
+        _mx_check((("hq", hq, h // 2), ("W2q", W2q, w // 2)), (("hs", hs, h // 32), ("w2s", w2s, w // 32)),
+                  (("offsets", offsets, _i32, E + 1), ("y_perm", y_perm, _bf16, rows * d)))
+    _on_gpu(stream, (hq, hs, offsets, W2q, w2s, y_perm, ws))
     _check(load().moe_expert_down_mxfp4(ctypes.byref(p), _ptr(hq), _ptr(hs), _ptr(offsets), _ptr(W2q), _ptr(w2s),
                                         _ptr(y_perm), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_forward_mxfp4(p, x, Wg, bg, W1q, w1s, W2q, w2s, y, logits=None, info=None, ws=None, stream=None):
     """The layer with MXFP4 experts."""
+    if not _packed:
+        _fill_packed()
     T, d, E, F = p.T, p.d, p.E, p.F
-    n1 = 2 * F if p.act == MOE_ACT_SWIGLU else F
-    _mx_check((("W1q", W1q, E * n1 * d // 2), ("W2q", W2q, E * d * F // 2)),
-              (("w1s", w1s, E * n1 * d // 32), ("w2s", w2s, E * d * F // 32)),
-              (("x", x, _bf16, T * d), ("Wg", Wg, _bf16, E * d), ("bg", bg, _f32, E), ("y", y, _bf16, T * d),
-               ("logits", logits, _f32, T * E)))
+    n, w1, w2 = T * d, E * (2 * F if p.act == MOE_ACT_SWIGLU else F) * d, E * d * F
+    try:
+        fits = (_mx_fits(((W1q, w1 // 2), (W2q, w2 // 2)), ((w1s, w1 // 32), (w2s, w2 // 32)))
+                and x.dtype is _bf16 and y.dtype is _bf16 and x.numel() >= n and y.numel() >= n
+                and (Wg is None or Wg.dtype is _bf16 and Wg.numel() >= E * d)
+                and (bg is None or bg.dtype is _f32 and bg.numel() >= E)
+                and (logits is None or logits.dtype is _f32 and logits.numel() >= T * E))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _mx_check((("W1q", W1q, w1 // 2), ("W2q", W2q, w2 // 2)), (("w1s", w1s, w1 // 32), ("w2s", w2s, w2 // 32)),
+                  (("x", x, _bf16, n), ("Wg", Wg, _bf16, E * d), ("bg", bg, _f32, E), ("y", y, _bf16, n),
+                   ("logits", logits, _f32, T * E)))
+    ri, extra = None, ()
     if info:
         least, choices = {"counts": E, "offsets": E + 1}, T * p.k
-        _mx_check(others=[(f, info.get(f), _f32 if f == "topk_w" else _i32, least.get(f, choices)) for f in _INFO])
-    _on_gpu(stream, x=x, Wg=Wg, bg=bg, W1q=W1q, w1s=w1s, W2q=W2q, w2s=w2s, y=y, logits=logits, ws=ws,
-            **{f: info.get(f) for f in _INFO} if info else {})
-    ri = _route_info(info) if info else None
+        extra = tuple(info.get(f) for f in _INFO)
+        for f, t in zip(_INFO, extra):
+            if t is not None and not isinstance(t, int):
+                of, m = _f32 if f == "topk_w" else _i32, least.get(f, choices)
+                if t.dtype is not of or t.numel() < m:
+                    _refuse(((f, t, of),), ((f, t, m),))
+        ri = _route_info(info)
+    _on_gpu(stream, (x, Wg, bg, W1q, w1s, W2q, w2s, y, logits, ws) + extra)
     _check(load().moe_forward_mxfp4(ctypes.byref(p), _ptr(x), _ptr(Wg), _ptr(bg), _ptr(W1q), _ptr(w1s), _ptr(W2q),
                                     _ptr(w2s), _ptr(y), _ptr(logits), ctypes.byref(ri) if ri is not None else None,
                                     _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -663,7 +708,7 @@ def moe_orthogonalize(grad, out, momentum=None, beta=0.95, nesterov=True, steps=
     rows, cols = grad.shape[-2:]
     count, n = (grad.shape[0] if grad.dim() == 3 else 1), grad.numel()
     _refuse((("out", out, _bf16), ("momentum", momentum, _f32)), (("out", out, n), ("momentum", momentum, n)))
-    _on_gpu(stream, grad=grad, out=out, momentum=momentum, ws=ws)
+    _on_gpu(stream, (grad, out, momentum, ws))
     _check(load().moe_orthogonalize(_ptr(grad), dt, _ptr(momentum), float(beta),
                                     int(bool(nesterov) and momentum is not None), count, rows, cols, int(steps),
                                     _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)))

@@ -256,6 +256,17 @@ def test_bindings_refuse_host_tensors(fn):
         getattr(moe, fn)(**calls(torch)[fn], stream=0)
 
 
+@pytest.mark.parametrize("fn", list(calls(pytest.importorskip("torch"))))
+def test_bindings_as_a_process_first_call(fn, monkeypatch):
+    """Before any call has looked up the element types."""
+    torch = pytest.importorskip("torch")
+    for name in ("_f32", "_i32", "_bf16", "_codes"):
+        monkeypatch.setattr(moe, name, None)
+    monkeypatch.setattr(moe, "_packed", ())
+    with pytest.raises(ValueError, match="GPU"):
+        getattr(moe, fn)(**calls(torch)[fn], stream=0)
+
+
 def test_bindings_pass_plain_addresses():
     """Plain addresses reach the library, which refuses the workspace or the address."""
     torch = pytest.importorskip("torch")
