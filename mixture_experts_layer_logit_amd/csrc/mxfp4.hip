@@ -76,16 +76,16 @@ constexpr int kMxMaxParts = 16;     // K parts of a tail tile
 constexpr int kMxSplitSlots = 256;  // partial tiles the workspace holds
 constexpr int kMxMinPart = 4;       // slices of a part
 
-typedef TileShape<256, 2, 4, 2, 8, 256, 1, true> LargeShape;
-typedef TileShape<128, 2, 4, 3, 8, 256, 1, true> Shape128;
-typedef TileShape<96, 1, 4, 3, 4, 256, 1, true> MediumShape;
-typedef TileShape<64, 1, 4, 3, 4, 256, 1, true> SmallShape;
-typedef TileShape<64, 2, 2, 3, 4, 128, 2, true> NarrowShape;
+typedef TileShape<256, 2, 4, 2, 8, 256, 1, 2> LargeShape;
+typedef TileShape<128, 2, 4, 3, 8, 256, 1, 2> Shape128;
+typedef TileShape<96, 1, 4, 3, 4, 256, 1, 2> MediumShape;
+typedef TileShape<64, 1, 4, 3, 4, 256, 1, 2> SmallShape;
+typedef TileShape<64, 2, 2, 3, 4, 128, 2, 1> NarrowShape;
 
-// Experts that a shape's tile counts have room for: two blocks of NarrowShape share a
-// CU's 160 KB of LDS.
+// Experts that a shape's tile counts have room for in what its stages leave of a CU's
+// 160 KB of LDS (two blocks of NarrowShape share them).
 template <typename S>
-constexpr int kMxMaxE = S::kPerCu > 1 ? 768 : kGemmMaxE;
+constexpr int kMxMaxE = S::kPerCu > 1 ? 768 : S::BM == 128 ? 1008 : kGemmMaxE;
 
 struct MxOp {
     template <int BYTE>
@@ -220,7 +220,7 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body uses device-only types; the host pass needs the stub only
     static_assert(2 * (S::WM * 32) * S::BN * 4 <= S::S * S::kStage, "two staged row fragments fit the stages");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
     __shared__ int32_t s_pref[kMxMaxE<S> + 1];
     __shared__ int32_t s_wsum[S::kWaves];
     const int tid = threadIdx.x;
@@ -254,8 +254,8 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
         if (item >= full) {
             const int j = item - full, part = j / tail;
             tile = full + j % tail;
-            k0 = part * nk / parts;
-            k1 = (part + 1) * nk / parts;
+            k0 = part * nk / parts / 2 * 2;
+            k1 = part + 1 < parts ? (part + 1) * nk / parts / 2 * 2 : nk;
             slot = (j % tail) * parts + part;
         }
         const TileDec t = decode_tile<S>(tile, s_pref, g.offsets, g.E, g.max_rows, ntn, tile_cols);
@@ -293,22 +293,21 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
         const uint32_t voffW = (uint32_t)lrow * (uint32_t)pitch + lchunk;
         const uint32_t voffW1 = second ? voffW : 0xf0000000u, row0 = (uint32_t)t.n0 * (uint32_t)pitch;
         const uint32_t row1 = second ? half1 * (uint32_t)pitch : 0, step = S::kRows * S::kWaves * (uint32_t)pitch;
-        // scale groups of this wavefront, the two dwords of 32 rows each, A's rows first;
-        // where they do not come out even, a wavefront repeats another's load
+        // this wavefront's loads of a scale unit: A's rows, then the tile's rows of W
         uint32_t voffS[S::kBlkS];
         i32x4 rsS[S::kBlkS];
-        const uint32_t cutS = lane & 1 ? 0xf0000000u : 0;
+        constexpr int kLanes = 64 / S::kSclRows;  // lanes of a row
 #pragma unroll
         for (int q = 0; q < S::kBlkS; ++q) {
-            const int group = (wave + q * S::kWaves) % S::kSclGroups;
-            const int r = group * 32 + lane / 2 - (group < S::kSclGroupsA ? 0 : S::BM);
-            const bool a = group < S::kSclGroupsA;
+            const int group = wave + q * S::kWaves;
+            const bool a = group * S::kSclRows < S::kSclA;
+            const int r = group * S::kSclRows + lane / kLanes - (a ? 0 : S::kSclA);
             const uint8_t* base = a ? g.As + rowA * spitch : g.Ws + (size_t)t.e * g.Nw * spitch;
             rsS[q] = make_rsrc(base, (a ? rowsA : (uint32_t)g.Nw) * (uint32_t)spitch);
             int src = a ? source(r) : r < S::kHalf ? t.n0 + r : (int)half1 + r - S::kHalf;
-            if (!a && src >= g.Nw)
+            if (!a && (r >= S::BN || src >= g.Nw))
                 src = -1;
-            voffS[q] = src >= 0 ? (uint32_t)src * (uint32_t)spitch + 4 * (lane & 1) : 0xf0000000u;
+            voffS[q] = src >= 0 ? (uint32_t)src * (uint32_t)spitch + lane % kLanes * 4 : 0xf0000000u;
         }
         // Small tiles, which stream weights: every tile of columns starts at another
         // slice, so that blocks which read rows a power of two apart at a time do not
@@ -318,38 +317,66 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
         int rot = 0;
         if (kRotate && pitch >= 4096 && pitch % 2048 == 0)
             rot = (t.n0 / tile_cols * 5) % (k1 - k0);
+        if (S::kUnit == 2 && (k1 - rot) % 2)  // the first slice follows the last at the border of a unit
+            rot ^= rot > 0;
 
-        auto issue = [&](int q, int st, int n0, int n1) {
-            const uint32_t at = lds0 + st * S::kStage, dst = at + wave * 1024;
-            int kb = q;
-            if constexpr (kRotate)
-                kb = q + rot >= k1 ? q + rot - (k1 - k0) : q + rot;
-            const uint32_t soff = (uint32_t)kb * S::RB, cut = kb == ragged ? 0xffffffffu : 0;
+        struct Loads {
+            const i32x4 &rsA, &rsW;
+            const i32x4 (&rsS)[S::kBlkS];
+            const uint32_t (&voffA)[S::kBlkA], (&voffS)[S::kBlkS];
+            uint32_t voffW, voffW1, row0, row1, step, lds0, cutA;
+            int keepS, wave, k0, k1, rot, last;
+            __device__ __forceinline__ int slice_of(int q) const
+            {
+                if constexpr (S::kWaves == 4)
+                    return q + rot >= k1 ? q + rot - (k1 - k0) : q + rot;
+                return q;
+            }
+            __device__ __forceinline__ void issue(int q, int st, int n0, int n1) const
+            {
+                const uint32_t dst = lds0 + st * S::kStage + wave * 1024;
+                const int kb = slice_of(q);
+                const uint32_t soff = (uint32_t)kb * S::RB, cut = kb == last ? 0xffffffffu : 0;
 #pragma unroll
-            for (int p = 0; p < S::kLoads; ++p) {
-                if (p < n0 || p >= n1)
-                    continue;
-                if (p < S::kBlkW / 2)
-                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW, soff + row0 + p * step);
-                else if (p < S::kBlkW)
-                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == MXEPI_SWIGLU ? voffW : voffW1,
-                          soff + row1 + (p - S::kBlkW / 2) * step);
-                else if (p < S::kBlkW + S::kBlkS) {
-                    const int s = p - S::kBlkW;
-                    dma4(rsS[s], at + S::kLdsA + S::kLdsW + (wave + s * S::kWaves) % S::kSclGroups * 256,
-                         voffS[s] | (cutS & cut), (uint32_t)kb * 8);
-                } else {
-                    const int a = p - S::kBlkW - S::kBlkS;
-                    dma16(rsA, dst + S::kWaves * a * 1024, voffA[a] | (cutA & cut), soff);
+                for (int p = 0; p < S::kLoads; ++p) {
+                    if (p < n0 || p >= n1)
+                        continue;
+                    if (p < S::kBlkW / 2)
+                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW, soff + row0 + p * step);
+                    else if (p < S::kBlkW)
+                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == MXEPI_SWIGLU ? voffW : voffW1,
+                              soff + row1 + (p - S::kBlkW / 2) * step);
+                    else
+                        dma16(rsA, dst + S::kWaves * (p - S::kBlkW) * 1024, voffA[p - S::kBlkW] | (cutA & cut), soff);
                 }
             }
+            __device__ __forceinline__ void scales(int q0, int place, uint32_t on) const
+            {
+                const uint32_t dst = lds0 + S::S * S::kStage + place * S::kSclUnit;
+                const uint32_t soff = (uint32_t)slice_of(q0) * 8;
+#pragma unroll
+                for (int q = 0; q < S::kBlkS; ++q) {
+                    const int group = wave + q * S::kWaves;
+                    if constexpr (S::kUnit == 2)
+                        dma16_if(S::kSclGroups % S::kWaves == 0 || group < S::kSclGroups ? on : 0u, rsS[q],
+                                 dst + group * 1024, voffS[q], soff);
+                    else if (S::kSclGroups % S::kWaves == 0 || group < S::kSclGroups)
+                        dma4(rsS[q], dst + group * 256, voffS[q], soff);
+                }
+            }
+            // the last slice's second half may be missing: its codes of A are zeros, and
+            // its scales, whatever lies there, must not be NaN.  (No row that is rotated
+            // ends in half a slice: the last one stays the last.)
+            __device__ __forceinline__ int keep(int q) const { return q == last ? keepS : -1; }
         };
+        const Loads loads = {rsA,  rsW,  rsS,  voffA, voffS, voffW, voffW1, row0, row1, step, lds0,
+                             cutA, (lane >> 5) - 1, wave, k0, k1, rot, ragged};
 
         wait_vmcnt<0>();  // the previous tile's stores are out of the count
         __syncthreads();  // and every wave is done with its LDS
         f32x16 acc[S::kFM][S::kFN];
         const int live = min(max((t.rows - wm * S::kWaveM + 31) / 32, 0), S::kFM);
-        tile_product<S, MxOp>(acc, lds, wm, wn, live, k0, k1, issue);
+        tile_product<S, MxOp>(acc, lds, wm, wn, live, k0, k1, loads);
         if (slot < 0) {
 #pragma unroll
             for (int i = 0; i < S::kFM; ++i) {
@@ -571,7 +598,7 @@ extern "C" hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uin
         auto most = [&](int bm) { return (busy == 1 ? (max_rows + bm - 1) / bm : max_rows / bm + busy) * ntn; };
         if (most(MediumShape::BM) <= ncu)
             return launch_epi<MediumShape>(epi, g, ncu, stream);
-        if (most(Shape128::BM) <= ncu)
+        if (most(Shape128::BM) <= ncu && E <= kMxMaxE<Shape128>)
             return launch_epi<Shape128>(epi, g, ncu, stream);
         return launch_epi<LargeShape>(epi, g, ncu, stream);
     }

@@ -237,8 +237,8 @@ struct NsOp {
     }
 };
 
-typedef TileShape<256, 2, 4, 2, 4, 256, 1, false> NsLarge;
-typedef TileShape<128, 2, 2, 2, 8, 128, 2, false> NsSmall;
+typedef TileShape<256, 2, 4, 2, 4, 256, 1, 0> NsLarge;
+typedef TileShape<128, 2, 2, 2, 8, 128, 2, 0> NsSmall;
 
 // The tiles of a product: `full` of them in one piece, the others, fewer than blocks run
 // at a time, in `parts` parts along K, whose sums moe_ns_tail_kernel adds.
@@ -526,7 +526,7 @@ void moe_ns_product_kernel(NsArgs g, NsPlan plan, NsStep st)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     static_assert(S::BM * S::BN * 2 <= S::S * S::kStage, "the staged output tile fits the stages");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::S * S::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
     const int M = MODE == NS_UPDATE ? g.n : g.m, pitch = 2 * (MODE == NS_GRAM ? g.np : g.mp), nk = pitch / S::RB;
     // an XCD's blocks take neighbouring tiles; the parts of split ones come last
     int item = blockIdx.x, k0 = 0, k1 = nk, slot = -1;
@@ -575,21 +575,28 @@ void moe_ns_product_kernel(NsArgs g, NsPlan plan, NsStep st)
         const int r = lrow + S::kRows * S::kWaves * i;
         voffW[i] = r < rowsW ? (uint32_t)r * (uint32_t)pitch + lchunk : 0xf0000000u;
     }
-    auto issue = [&](int q, int stage, int n0, int n1) {
-        const uint32_t dst = lds0 + stage * S::kStage + wave * 1024, soff = (uint32_t)q * S::RB;
+    struct Loads {
+        const i32x4 &rsA, &rsW;
+        const uint32_t (&voffA)[S::kBlkA], (&voffW)[S::kBlkW];
+        uint32_t lds0;
+        __device__ __forceinline__ void issue(int q, int stage, int n0, int n1) const
+        {
+            const uint32_t dst = lds0 + stage * S::kStage, soff = (uint32_t)q * S::RB;
 #pragma unroll
-        for (int p = 0; p < S::kLoads; ++p) {
-            if (p < n0 || p >= n1)
-                continue;
-            if (p < S::kBlkW)
-                dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW[p], soff);
-            else
-                dma16(rsA, dst + S::kWaves * (p - S::kBlkW) * 1024, voffA[p - S::kBlkW], soff);
+            for (int p = 0; p < S::kLoads; ++p) {
+                if (p < n0 || p >= n1)
+                    continue;
+                if (p < S::kBlkW)
+                    dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW[p], soff);
+                else
+                    dma16(rsA, dst + S::kWaves * (p - S::kBlkW) * 1024, voffA[p - S::kBlkW], soff);
+            }
         }
     };
+    const Loads loads = {rsA, rsW, voffA, voffW, lds0 + wave * 1024};
     f32x16 acc[S::kFM][S::kFN];
     const int live = min(max((rowsA - wm * S::kWaveM + 31) / 32, 0), S::kFM);
-    tile_product<S, NsOp>(acc, lds, wm, wn, live, k0, k1, issue);
+    tile_product<S, NsOp>(acc, lds, wm, wn, live, k0, k1, loads);
     if (slot < 0) {
         ns_store<S, MODE, S::kFM>(g, st, mat, ti, tj, 0, acc, lds);
         return;

@@ -14,13 +14,14 @@ namespace moe {
 // Block tile BM x BN, WM x WN wavefronts, S stages.  The BN rows of W are two halves;
 // a wavefront takes the same rows of both, so that a gate and an up value of a hidden
 // column meet in one lane.  GM: m-tiles of a group that share W's columns (decode_tile).
-// SCALES: behind the rows lie two dwords of scales of each, one for either half of its
-// 128 bytes.
-template <int BM_, int WM_, int WN_, int S_, int GM_, int BN_, int PER_CU_, bool SCALES_>
+// UNIT: the operands have scales, 8 bytes for the 128 of a row and slice, which lie behind
+// the stages: those of two slices in two places in turn (2), or a slice's in a place for
+// each stage (1).
+template <int BM_, int WM_, int WN_, int S_, int GM_, int BN_, int PER_CU_, int UNIT_>
 struct TileShape {
     static constexpr int BM = BM_, BN = BN_, kHalf = BN / 2, kPerCu = PER_CU_;
     static constexpr int WM = WM_, WN = WN_, S = S_, GM = GM_, RB = 128;
-    static constexpr bool kScales = SCALES_;
+    static constexpr int kUnit = UNIT_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int kWavesPerSimd = kWaves / 4 * kPerCu;
     static constexpr int kWaveM = BM / WM, kWaveN = BN / WN;
@@ -28,11 +29,14 @@ struct TileShape {
     static constexpr int kHalfN = kWaveN / 2, kHalfF = kFN / 2;
     static constexpr int kRows = 1024 / RB;  // tile rows of a 1 KB load
     static constexpr int kLdsA = BM * RB, kLdsW = BN * RB;
-    static constexpr int kSclGroupsA = kScales ? BM / 32 : 0, kSclGroups = kScales ? (BM + BN) / 32 : 0;  // of 64 dwords
+    // a load of scales takes 16 bytes (UNIT 2) or 4 a lane, of kSclRows rows of one operand
+    static constexpr int kSclRows = kUnit == 2 ? 64 : 32, kSclA = (BM + kSclRows - 1) / kSclRows * kSclRows;
+    static constexpr int kSclGroups = kUnit ? (kSclA + BN) / kSclRows : 0;
     static constexpr int kBlkS = (kSclGroups + kWaves - 1) / kWaves;
-    static constexpr int kStage = kLdsA + kLdsW + kSclGroups * 256;
+    static constexpr int kSclUnit = kSclGroups * kSclRows * 8 * kUnit, kSclUnits = kUnit == 1 ? S : 2;
+    static constexpr int kStage = kLdsA + kLdsW, kLds = S * kStage + kSclUnits * kSclUnit;
     static constexpr int kBlkA = BM / kRows / kWaves, kBlkW = BN / kRows / kWaves;  // loads per wavefront and stage
-    static constexpr int kLoads = kBlkA + kBlkW + kBlkS;
+    static constexpr int kLoads = kBlkA + kBlkW;
     static constexpr int kTileFloats = BM * BN;
     static_assert(kFN % 2 == 0, "a wavefront takes rows of both halves of W");
     static_assert(kWaves % 4 == 0 && BM % (kRows * kWaves) == 0, "loads split evenly");
@@ -59,10 +63,26 @@ __device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds, uint32_t v
                      : "memory");
 }
 
-// The K loop over slices [k0, k1) (each 128 bytes of K) for a wavefront whose first L
+// dma16 for a wavefront whose lanes are all active, where `on` is all ones, or, where it is 0,
+// nothing: a condition without a branch, which would split a loop that is scheduled as a
+// whole.
+__device__ __forceinline__ void dma16_if(uint32_t on, const i32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff)
+{
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds), mask = __builtin_amdgcn_readfirstlane(on);
+    uint32_t so = __builtin_amdgcn_readfirstlane(soff);
+    __asm__("" : "+s"(so));
+    __asm__ volatile("s_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\ts_mov_b32 m0, %0\n\t"
+                     "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
+                     :
+                     : "s"(m0), "v"(voff), "s"(rsrc), "s"(so), "s"(mask)
+                     : "memory");
+}
+
+// The K loop over slices [k0, k1) (k0 a multiple of UNIT) (each 128 bytes of K) for a wavefront whose first L
 // row fragments hold rows that count (the others are neither read nor multiplied).
 // issue(q, st, n0, n1) starts loads [n0, n1) of the kLoads of slice q into stage st,
-// W's first.
+// W's first; scales(q, place, on) those of the scales from slice q on, if on; keep(q) is a mask that
+// clears the scales of what is missing of slice q (only of the last one).
 //
 // Lane l of a 32-row fragment reads the chunks 4 (l / 32) .. + 3 of its row, one per
 // matrix instruction: two chunks in each of a slice's two k-steps.  Which values of K
@@ -73,17 +93,21 @@ __device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds, uint32_t v
 // them; behind a barrier the stage is free then and takes the loads of slice kt + S.
 // Between the two k-steps slice kt + 1 has to be there (a second barrier), so a load
 // has 1 1/4 slices (S = 2) to arrive.
-template <typename S, typename Op, int L, typename Issue>
+template <typename S, typename Op, int L, typename Loads>
 __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const uint8_t* lds, int wm, int wn, int k0,
-                                           int k1, const Issue& issue)
+                                           int k1, const Loads& loads)
 {
     constexpr int kHalfF = S::kHalfF;
     constexpr int NI = L * S::kFN, kNI = NI > 0 ? NI : 1, NM = 2 * NI, NR = L > 0 ? 2 * (L + S::kFN) : 0;
     const int lane = lane_id();
     const uint32_t rdA = tile_at(wm * S::kWaveM + (lane & 31), 4 * (lane >> 5));
     const uint32_t rdW = S::kLdsA + tile_at(wn * S::kHalfN + (lane & 31), 4 * (lane >> 5));
-    const uint32_t scl = S::kLdsA + S::kLdsW + 8 * (lane & 31) + 4 * (lane >> 5);
-    const uint32_t scA = scl + 8 * wm * S::kWaveM, scW = scl + 8 * (S::BM + wn * S::kHalfN);
+    constexpr int kPitch = 8 * S::kUnit;  // bytes of a row's scales in a unit
+    const uint32_t scl = S::S * S::kStage + kPitch * (lane & 31) + 4 * (lane >> 5);
+    const uint32_t scA = scl + kPitch * wm * S::kWaveM, scW = scl + kPitch * (S::kSclA + wn * S::kHalfN);
+    auto scales_at = [&](int q, int stage) {  // where slice q's scales lie
+        return S::kUnit == 2 ? (q >> 1 & 1) * S::kSclUnit + (q & 1) * 8 : stage * S::kSclUnit;
+    };
     struct Frags {
         i32x4 w[2][S::kFN], a[2][S::kFM];
     };
@@ -100,34 +124,57 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
         else
             nx.a[h][n - S::kFN] = v;
     };
-    auto read_a_scale = [&](int i, uint32_t st) {
-        if constexpr (S::kScales)
-            sa[i] = *reinterpret_cast<const int*>(lds + st + scA + i * 256);
+    auto read_a_scale = [&](int i, uint32_t at) {
+        if constexpr (S::kUnit)
+            sa[i] = *reinterpret_cast<const int*>(lds + at + scA + i * 32 * kPitch);
     };
-    auto read_w_scales = [&](uint32_t st) {
-        if constexpr (S::kScales)
+    auto read_w_scales = [&](uint32_t at) {
+        if constexpr (S::kUnit)
 #pragma unroll
             for (int j = 0; j < S::kFN; ++j)
-                swn[j] = *reinterpret_cast<const int*>(lds + st + scW +
-                                                       8 * ((j / kHalfF) * S::kHalf + (j % kHalfF) * 32));
+                swn[j] = *reinterpret_cast<const int*>(lds + at + scW +
+                                                       kPitch * ((j / kHalfF) * S::kHalf + (j % kHalfF) * 32));
+    };
+    auto cut_scales = [&](int q) {
+        if constexpr (S::kUnit) {
+            const int keep = loads.keep(q);
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                sa[i] &= keep;
+#pragma unroll
+            for (int j = 0; j < S::kFN; ++j)
+                sw[j] &= keep;
+        }
     };
     // One k-step: the matrix instructions on the fragments in f, and between them the
     // LDS reads of the next k-step's fragments into nx (k-step kk of stage st) and,
-    // where LAST, the scales of the next slice; where LOADS, the loads of slice q into
-    // stage lst.  A matrix instruction runs for 32 cycles, in which its wavefront can
+    // where LAST, the scales of slice q + 1 (at sc); where LOADS, the loads of slice q + S
+    // into stage lst, and of scales.  A matrix instruction runs for 32 cycles, in which its wavefront can
     // issue the few instructions that follow it.
+    // In slice q's second k-step its own scales have been read by every wavefront, so their
+    // place is free once the slice's unit ends; what is loaded here is read S - 1 or more
+    // slices' loads later, behind a wait that leaves fewer than those in flight.  Behind the
+    // last slice it is not read at all.
+    auto next_scales = [&](int q, int stage) {
+        if constexpr (S::kUnit == 2)
+            loads.scales(q + 3, (q + 3) >> 1 & 1, -(uint32_t)(q & 1));
+        if constexpr (S::kUnit == 1)
+            loads.scales(q + S::S, stage, ~0u);
+    };
     constexpr int kEarly = S::kBlkW;  // loads issued in a slice's first k-step: W's
     constexpr int kFree = NM >= 16 ? 6 : NM > 2 ? NM / 2 : NM;     // instructions behind which its reads are spread
     constexpr int kBar = NM >= 16 ? 6 : NM > 0 ? kFree - 1 : 0;    // the one behind which the stage is free
-    auto kstep = [&](const Frags& f, Frags& nx, uint32_t st, int kk, auto last, auto loads, int q, int lst) {
-        constexpr bool LAST = decltype(last)::value, LOADS = decltype(loads)::value;
+    auto kstep = [&](const Frags& f, Frags& nx, uint32_t st, int kk, uint32_t sc, auto last, auto more, int q, int lst) {
+        constexpr bool LAST = decltype(last)::value, LOADS = decltype(more)::value;
         constexpr int kOver = LAST ? NM : kFree;
         constexpr int kPer = kOver > 0 && (NR + kOver - 1) / kOver > 1 ? (NR + kOver - 1) / kOver : 1;
         if constexpr (NM == 0) {
             if (!LAST && LOADS)
                 lds_barrier();
             if (LOADS)
-                issue(q, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
+                loads.issue(q + S::S, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
+            if constexpr (LAST && LOADS)
+                next_scales(q, lst);
         }
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
@@ -141,19 +188,22 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
                     read(r, nx, st, kk);
             if constexpr (LAST) {
                 if (h == 1 && j == S::kFN - 1)
-                    read_a_scale(i, st);
+                    read_a_scale(i, sc);
                 if (m == 0)
-                    read_w_scales(st);
+                    read_w_scales(sc);
+                if constexpr (LOADS)
+                    if (m == 1)
+                        next_scales(q, lst);
                 constexpr int kLate = S::kLoads - kEarly, kSafe = NM > 0 ? NM : 1;
                 if constexpr (LOADS)
-                    issue(q, lst, kEarly + m * kLate / kSafe, kEarly + (m + 1) * kLate / kSafe);
+                    loads.issue(q + S::S, lst, kEarly + m * kLate / kSafe, kEarly + (m + 1) * kLate / kSafe);
             } else if constexpr (LOADS) {
                 // every wavefront's reads of the stage are done: it is free
                 if (m == kBar)
                     lds_barrier();
                 if (m >= kBar) {
                     constexpr int kLeft = NM - kBar > 0 ? NM - kBar : 1;
-                    issue(q, lst, (m - kBar) * kEarly / kLeft, (m - kBar + 1) * kEarly / kLeft);
+                    loads.issue(q + S::S, lst, (m - kBar) * kEarly / kLeft, (m - kBar + 1) * kEarly / kLeft);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -171,23 +221,26 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
             if (r / kPer == m)
                 read(r, f0, 0, 0);
         if (m >= NI && m % S::kFN == S::kFN - 1)
-            read_a_scale(m % kNI / S::kFN, 0);
+            read_a_scale(m % kNI / S::kFN, scales_at(k0, 0));
         if (m == 0)
-            read_w_scales(0);
+            read_w_scales(scales_at(k0, 0));
         __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < S::kFN; ++j)
         sw[j] = swn[j];
     int cur = 0;  // stage of slice kt
-    auto slice = [&](int kt, auto loads) {
-        constexpr bool LOADS = decltype(loads)::value;
+    auto slice = [&](int kt, auto more) {
+        constexpr bool LOADS = decltype(more)::value;
         const int nxt = cur + 1 == S::S ? 0 : cur + 1;
-        kstep(f0, f1, cur * S::kStage, 1, no, loads, kt + S::S, cur);
-        // slice kt + 1 has to be there
+        if constexpr (!LOADS)
+            cut_scales(kt);
+        kstep(f0, f1, cur * S::kStage, 1, 0, no, more, kt, cur);
+        // slice kt + 1 has to be there (scales among the newer loads only make the wait
+        // stricter)
         wait_vmcnt<LOADS ? (S::S - 2) * S::kLoads + kEarly : 0>();
         lds_barrier();
-        kstep(f1, f0, nxt * S::kStage, 0, yes, loads, kt + S::S, cur);
+        kstep(f1, f0, nxt * S::kStage, 0, scales_at(kt + 1, nxt), yes, more, kt, cur);
 #pragma unroll
         for (int j = 0; j < S::kFN; ++j)
             sw[j] = swn[j];
@@ -203,9 +256,9 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
 // All of a tile's K: the first stages' loads, and the loop for the `live` row
 // fragments of this wavefront (a copy of it for each count).  Every earlier access to
 // the stages has to be behind a barrier.
-template <typename S, typename Op, typename Issue>
+template <typename S, typename Op, typename Loads>
 __device__ __forceinline__ void tile_product(f32x16 (&acc)[S::kFM][S::kFN], const uint8_t* lds, int wm, int wn,
-                                             int live, int k0, int k1, const Issue& issue)
+                                             int live, int k0, int k1, const Loads& loads)
 {
 #pragma unroll
     for (int i = 0; i < S::kFM; ++i)
@@ -214,25 +267,30 @@ __device__ __forceinline__ void tile_product(f32x16 (&acc)[S::kFM][S::kFN], cons
 #pragma unroll
             for (int v = 0; v < 16; ++v)
                 acc[i][j][v] = 0.0f;
+    if constexpr (S::kUnit)
+#pragma unroll
+        for (int u = 0; u < S::kSclUnits; ++u)
+            if (k0 + u * S::kUnit < k1)
+                loads.scales(k0 + u * S::kUnit, S::kUnit == 2 ? ((k0 >> 1) + u) & 1 : u, ~0u);
 #pragma unroll
     for (int q = 0; q < S::S; ++q)
         if (k0 + q < k1)
-            issue(k0 + q, q, 0, S::kLoads);
+            loads.issue(k0 + q, q, 0, S::kLoads);
     if (k1 - k0 >= S::S)
         wait_vmcnt<(S::S - 1) * S::kLoads>();
     else
         wait_vmcnt<0>();
     lds_barrier();
     if (S::kFM == 1 || live >= S::kFM)
-        tile_kloop<S, Op, S::kFM>(acc, lds, wm, wn, k0, k1, issue);
+        tile_kloop<S, Op, S::kFM>(acc, lds, wm, wn, k0, k1, loads);
     else if (S::kFM > 3 && live == 3)
-        tile_kloop<S, Op, (S::kFM > 3 ? 3 : 1)>(acc, lds, wm, wn, k0, k1, issue);
+        tile_kloop<S, Op, (S::kFM > 3 ? 3 : 1)>(acc, lds, wm, wn, k0, k1, loads);
     else if (S::kFM > 2 && live == 2)
-        tile_kloop<S, Op, (S::kFM > 2 ? 2 : 1)>(acc, lds, wm, wn, k0, k1, issue);
+        tile_kloop<S, Op, (S::kFM > 2 ? 2 : 1)>(acc, lds, wm, wn, k0, k1, loads);
     else if (live == 1)
-        tile_kloop<S, Op, 1>(acc, lds, wm, wn, k0, k1, issue);
+        tile_kloop<S, Op, 1>(acc, lds, wm, wn, k0, k1, loads);
     else
-        tile_kloop<S, Op, 0>(acc, lds, wm, wn, k0, k1, issue);
+        tile_kloop<S, Op, 0>(acc, lds, wm, wn, k0, k1, loads);
     lds_barrier();
 }
 
