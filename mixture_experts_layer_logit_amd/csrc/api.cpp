@@ -72,7 +72,7 @@ hipError_t moe_launch_mxfp4_quantize(int dtype, const void* src, long long block
                                      hipStream_t stream);
 hipError_t moe_launch_mxfp4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, long long blocks,
                                        void* dst, hipStream_t stream);
-size_t moe_mxfp4_gemm_partial_bytes(int mean_rows);
+size_t moe_mxfp4_gemm_partial_bytes(int E, int K, int Nout, int glu, int max_rows, int mean_rows);
 hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uint8_t* As, const int32_t* gather, int gather_rows,
                                  const uint8_t* W, const uint8_t* Ws, uint8_t* Hq, uint8_t* Hs, void* Y,
                                  const int32_t* offsets, int E, int K, int Nw, int Nout, int F, int max_rows,
@@ -592,7 +592,9 @@ LayoutMxfp4 layout_mxfp4_of(const moe_problem* p)
     L.src_token = take(T * k * 4);
     L.chunk_cnt = take(std::max<size_t>(nchunks, 1) * E * 4);
     L.logits = take(T * E * 4);
-    L.partial = take(moe_mxfp4_gemm_partial_bytes(mean_rows_of(p)));
+    L.partial = take(std::max(
+        moe_mxfp4_gemm_partial_bytes(p->E, p->d, p->F, p->act == MOE_ACT_SWIGLU, p->T * p->k, mean_rows_of(p)),
+        moe_mxfp4_gemm_partial_bytes(p->E, p->F, p->d, 0, p->T * p->k, mean_rows_of(p))));
     L.xq = take(T * (d / 2));
     L.xs = take(T * (d / 32));
     L.hq = take(T * k * (F / 2));

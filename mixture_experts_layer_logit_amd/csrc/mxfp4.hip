@@ -6,6 +6,7 @@
 // consecutive values of K (a byte b stands for 2^(b - 127)):
 //   u[r, n] = sum_b 2^(sA[r, b] + sW[n, b] - 254) sum_{k in block b} a[r, k] w[n, k]
 #include <algorithm>
+#include <cmath>
 
 #include "common.h"
 #include "gemm_common.h"
@@ -76,16 +77,10 @@ constexpr int kMxMaxParts = 16;     // K parts of a tail tile
 constexpr int kMxSplitSlots = 256;  // partial tiles the workspace holds
 constexpr int kMxMinPart = 4;       // slices of a part
 
-typedef TileShape<256, 2, 4, 2, 8, 256, 1, 2> LargeShape;
-typedef TileShape<128, 2, 4, 3, 8, 256, 1, 2> Shape128;
-typedef TileShape<96, 1, 4, 3, 4, 256, 1, 2> MediumShape;
-typedef TileShape<64, 1, 4, 3, 4, 256, 1, 2> SmallShape;
-typedef TileShape<64, 2, 2, 3, 4, 128, 2, 1> NarrowShape;
-
-// Experts that a shape's tile counts have room for in what its stages leave of a CU's
-// 160 KB of LDS (two blocks of NarrowShape share them).
-template <typename S>
-constexpr int kMxMaxE = S::kPerCu > 1 ? 768 : S::BM == 128 ? 1008 : kGemmMaxE;
+// 256 x 256 with 8 wavefronts, or 128 x 128 with 4 and two blocks a CU, which hide each
+// other's waits.
+typedef TileShape<256, 2, 4, 2, 8, 256, 1, true> LargeShape;
+typedef TileShape<128, 2, 2, 2, 4, 128, 2, true> PairShape;
 
 struct MxOp {
     template <int BYTE>
@@ -219,9 +214,9 @@ __global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(S::
 void moe_mxfp4_gemm_kernel(MxGemmArgs g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body uses device-only types; the host pass needs the stub only
-    static_assert(2 * (S::WM * 32) * S::BN * 4 <= S::S * S::kStage, "two staged row fragments fit the stages");
+    static_assert((S::kFM > 1 ? 2 : 1) * (S::WM * 32) * S::BN * 4 <= S::S * S::kStage, "staged row fragments fit");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-    __shared__ int32_t s_pref[kMxMaxE<S> + 1];
+    __shared__ int32_t s_pref[kGemmMaxE + 1];
     __shared__ int32_t s_wsum[S::kWaves];
     const int tid = threadIdx.x;
     const int lane = lane_id();
@@ -293,31 +288,31 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
         const uint32_t voffW = (uint32_t)lrow * (uint32_t)pitch + lchunk;
         const uint32_t voffW1 = second ? voffW : 0xf0000000u, row0 = (uint32_t)t.n0 * (uint32_t)pitch;
         const uint32_t row1 = second ? half1 * (uint32_t)pitch : 0, step = S::kRows * S::kWaves * (uint32_t)pitch;
-        // this wavefront's loads of a scale unit: A's rows, then the tile's rows of W
+        // this wavefront's loads of scales: 64 rows of A, or of the tile's rows of W
         uint32_t voffS[S::kBlkS];
         i32x4 rsS[S::kBlkS];
-        constexpr int kLanes = 64 / S::kSclRows;  // lanes of a row
 #pragma unroll
         for (int q = 0; q < S::kBlkS; ++q) {
             const int group = wave + q * S::kWaves;
-            const bool a = group * S::kSclRows < S::kSclA;
-            const int r = group * S::kSclRows + lane / kLanes - (a ? 0 : S::kSclA);
+            const bool a = group * 64 < S::BM;
+            const int r = group * 64 + lane - (a ? 0 : S::BM);
             const uint8_t* base = a ? g.As + rowA * spitch : g.Ws + (size_t)t.e * g.Nw * spitch;
             rsS[q] = make_rsrc(base, (a ? rowsA : (uint32_t)g.Nw) * (uint32_t)spitch);
             int src = a ? source(r) : r < S::kHalf ? t.n0 + r : (int)half1 + r - S::kHalf;
-            if (!a && (r >= S::BN || src >= g.Nw))
+            if (!a && src >= g.Nw)
                 src = -1;
-            voffS[q] = src >= 0 ? (uint32_t)src * (uint32_t)spitch + lane % kLanes * 4 : 0xf0000000u;
+            voffS[q] = src >= 0 ? (uint32_t)src * (uint32_t)spitch : 0xf0000000u;
         }
-        // Small tiles, which stream weights: every tile of columns starts at another
-        // slice, so that blocks which read rows a power of two apart at a time do not
-        // meet in few of the memory's channels.  The tile decides, so the sums keep
-        // their order from run to run.
-        constexpr bool kRotate = S::kWaves == 4;
+        // Two blocks a CU, which stream weights where rows are few: every tile of columns
+        // starts at another slice, so that blocks which read rows a power of two apart at a
+        // time do not meet in few of the memory's channels.  The tile decides, so the sums
+        // keep their order from run to run.  The first slice follows the last behind an odd
+        // one.
+        constexpr bool kRotate = S::kPerCu > 1;
         int rot = 0;
         if (kRotate && pitch >= 4096 && pitch % 2048 == 0)
             rot = (t.n0 / tile_cols * 5) % (k1 - k0);
-        if (S::kUnit == 2 && (k1 - rot) % 2)  // the first slice follows the last at the border of a unit
+        if ((k1 - rot) % 2)
             rot ^= rot > 0;
 
         struct Loads {
@@ -328,7 +323,7 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
             int keepS, wave, k0, k1, rot, last;
             __device__ __forceinline__ int slice_of(int q) const
             {
-                if constexpr (S::kWaves == 4)
+                if constexpr (S::kPerCu > 1)
                     return q + rot >= k1 ? q + rot - (k1 - k0) : q + rot;
                 return q;
             }
@@ -355,14 +350,8 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
                 const uint32_t dst = lds0 + S::S * S::kStage + place * S::kSclUnit;
                 const uint32_t soff = (uint32_t)slice_of(q0) * 8;
 #pragma unroll
-                for (int q = 0; q < S::kBlkS; ++q) {
-                    const int group = wave + q * S::kWaves;
-                    if constexpr (S::kUnit == 2)
-                        dma16_if(S::kSclGroups % S::kWaves == 0 || group < S::kSclGroups ? on : 0u, rsS[q],
-                                 dst + group * 1024, voffS[q], soff);
-                    else if (S::kSclGroups % S::kWaves == 0 || group < S::kSclGroups)
-                        dma4(rsS[q], dst + group * 256, voffS[q], soff);
-                }
+                for (int q = 0; q < S::kBlkS; ++q)
+                    dma16_if(on, rsS[q], dst + (wave + q * S::kWaves) * 1024, voffS[q], soff);
             }
             // the last slice's second half may be missing: its codes of A are zeros, and
             // its scales, whatever lies there, must not be NaN.  (No row that is rotated
@@ -463,44 +452,69 @@ __global__ __launch_bounds__(S::kThreads) void moe_mxfp4_tail_kernel(MxGemmArgs 
 namespace {
 using namespace moe;
 
-constexpr int kLargeRows = 192;
+constexpr int kMxCus = 256;  // of gfx950
 
-// Whether the last round (at most kMxSplitSlots / 2 tiles of it) is split along K.  The
-// split costs a second launch (about 4 us), so it is left out where K is short, and
-// where the tiles expected (rows spread evenly over min(rows, E) experts) fill more
-// than half of the only round.
+// How a product is run: its tiles, and whether the last, partly filled round of them is
+// split along K.
+struct MxChoice {
+    bool large, split;
+    double us;
+};
+
+// Time in us on tiles of one shape, fitted to 118 sizes (1 to 2048 rows of 1 to 256 experts,
+// K 512 to 14336, both kinds of layer).  A tile takes 3.5 or 7 us and, a slice, 0.45 to 1.32
+// us (128 x 128) or 0.9 to 2.03 (256 x 256) with the share of its rows that exist and of
+// the blocks that run at a time (where some CUs run two, they set the time); a split round
+// takes 7 us more for its second launch; and no size is faster than its weights at 5.9
+// TB/s.  Experts hold about max(1, mean / BM +
+// 1/2) tiles of rows, for their rows are seldom even.  Measured, 128 x 128 / 256 x 256:
+//   SwiGLU, 8 experts, 4096 x 4096     1 row  24 /  25    96  28 / 30    256  55 / 71    512   98 / 100   2048  359 / 305
+//   plain, 8 experts, 14336 x 4096     8      41 /  48    96  53 / 61    256 108 / 112   512  178 / 183   2048  631 / 484
+//   SwiGLU, 8 experts, 14336 x 4096    1      89 /  94    128 149 / 111  256 208 / 222   512  352 / 285
+//   plain, 256 experts, 1024 x 512     8      17 /  19    96  24 / 27    256  42 /  45
+// 64-, 96- and 128-row tiles of 256 columns were at best 10 % faster than the better of the
+// two, at most sizes slower.
 template <typename S>
-bool split_pays(const MxGemmArgs& g, long long ntn, int blocks)
+MxChoice estimate(int E, int K, int Nout, bool glu, int max_rows, int mean_rows, bool split)
 {
-    if (g.K < 4096)
-        return false;
-    const long long busy = std::min(g.E, g.max_rows);
-    const long long tiles = busy * std::max(1ll, (g.max_rows / busy + S::BM - 1) / S::BM) * ntn;
-    return tiles <= std::min(blocks, kMxSplitSlots) / 2 || tiles > blocks;
+    const bool large = S::BM == 256;
+    const int nk = (K + kMxSlice - 1) / kMxSlice, cols = glu ? S::kHalf : S::BN, busy = std::min(E, max_rows);
+    const double mean = std::max(1, mean_rows);
+    const double mt = busy == 1 ? (max_rows + S::BM - 1) / S::BM : mean < 0.8 * S::BM ? 1.0 : mean / S::BM + 0.5;
+    const double tiles = busy * mt * ((Nout + cols - 1) / cols), slots = kMxCus * S::kPerCu, rows = std::min(1.0, mean / S::BM);
+    auto time = [&](double slices, double blocks) {
+        const double f = (blocks > kMxCus ? 1.0 : blocks / slots) * rows;
+        return large ? 7.0 + slices * (0.9 + 1.13 * f) : 3.5 + slices * (0.45 + 0.87 * f);
+    };
+    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots;
+    double tail = rest > 0.5 ? time(nk, rest) : 0.0;
+    const int parts = rest > 0.5 ? std::min(std::min(kMxMaxParts, (int)(kMxSplitSlots / rest)), nk / kMxMinPart) : 1;
+    MxChoice c = {large, false, 0.0};
+    if (split && parts > 1) {
+        const double t = 7.0 + time((double)nk / parts, rest * parts);
+        if (t < tail)
+            tail = t, c.split = true;
+    }
+    const double weights = (double)busy * (glu ? 2 : 1) * Nout * K * (0.5 + 1.0 / kMxBlk);
+    c.us = std::max(rounds * time(nk, slots) + tail, weights / 5.9e6);
+    return c;
 }
 
-bool narrow_pays(int mean_rows, long long tiles, int K, int ncu)
+MxChoice choose(int E, int K, int Nout, bool glu, int max_rows, int mean_rows, bool split)
 {
-    if (tiles <= ncu)
-        return true;
-    if (mean_rows >= kLargeRows)
-        return tiles <= 2 * ncu;
-    if (K < 4096)
-        return mean_rows <= 32 || tiles <= 2 * ncu;
-    return false;
+    const MxChoice l = estimate<LargeShape>(E, K, Nout, glu, max_rows, mean_rows, split);
+    const MxChoice p = estimate<PairShape>(E, K, Nout, glu, max_rows, mean_rows, split);
+    return l.us < 0.98 * p.us ? l : p;
 }
 
 template <typename S, int EPI>
-hipError_t launch_shape(MxGemmArgs g, int ncu, hipStream_t stream)
+hipError_t launch_shape(const MxGemmArgs& g, int ncu, hipStream_t stream)
 {
     const int tile_cols = EPI == MXEPI_SWIGLU ? S::kHalf : S::BN;
     const long long ntn = (g.Nout + tile_cols - 1) / tile_cols;
     // upper bound on m-tiles: whole tiles plus one partial per expert
     const long long mt = g.max_rows / S::BM + (long long)std::min(g.E, g.max_rows);
-    ncu *= S::kPerCu;
-    if (!split_pays<S>(g, ntn, ncu))
-        g.partial = nullptr;
-    long long grid = ncu;
+    long long grid = ncu * S::kPerCu;
     if (mt * ntn < grid && g.partial == nullptr)
         grid = (mt * ntn + 7) / 8 * 8;
     moe_mxfp4_gemm_kernel<S, EPI><<<dim3((unsigned)grid), dim3(S::kThreads), 0, stream>>>(g);
@@ -513,19 +527,13 @@ hipError_t launch_shape(MxGemmArgs g, int ncu, hipStream_t stream)
 }
 
 template <typename S>
-hipError_t launch_narrow(int epi, const MxGemmArgs& g, int ncu, hipStream_t s)
-{
-    if (epi == MXEPI_RELU)
-        return launch_shape<S, MXEPI_RELU>(g, ncu, s);
-    return epi == MXEPI_F32 ? launch_shape<S, MXEPI_F32>(g, ncu, s) : launch_shape<S, MXEPI_NONE>(g, ncu, s);
-}
-
-template <typename S>
 hipError_t launch_epi(int epi, const MxGemmArgs& g, int ncu, hipStream_t s)
 {
     if (epi == MXEPI_SWIGLU)
         return launch_shape<S, MXEPI_SWIGLU>(g, ncu, s);
-    return launch_narrow<S>(epi, g, ncu, s);
+    if (epi == MXEPI_RELU)
+        return launch_shape<S, MXEPI_RELU>(g, ncu, s);
+    return epi == MXEPI_F32 ? launch_shape<S, MXEPI_F32>(g, ncu, s) : launch_shape<S, MXEPI_NONE>(g, ncu, s);
 }
 
 template <typename ET>
@@ -572,10 +580,14 @@ extern "C" hipError_t moe_launch_mxfp4_dequantize(int dtype, const uint8_t* code
     return hipGetLastError();
 }
 
-// Bytes of the K split's partial tiles for this mean number of rows per expert.
-extern "C" size_t moe_mxfp4_gemm_partial_bytes(int mean_rows)
+// Bytes of the partial tiles of a product whose last round is split along K (0: it is not).
+// moe_launch_mxfp4_gemm chooses by the same sizes.
+extern "C" size_t moe_mxfp4_gemm_partial_bytes(int E, int K, int Nout, int glu, int max_rows, int mean_rows)
 {
-    return (size_t)kMxSplitSlots * 4 * (mean_rows >= kLargeRows ? LargeShape::kTileFloats : MediumShape::kTileFloats);
+    if (max_rows <= 0)
+        return 0;
+    const MxChoice c = choose(E, K, Nout, glu, max_rows, mean_rows, true);
+    return c.split ? (size_t)kMxSplitSlots * 4 * (c.large ? LargeShape::kTileFloats : PairShape::kTileFloats) : 0;
 }
 
 // epi 0: Y = bf16 rows, 3: Y = fp32 rows; 1 ReLU, 2 SwiGLU: Hq, Hs.  mean_rows:
@@ -587,23 +599,8 @@ extern "C" hipError_t moe_launch_mxfp4_gemm(int epi, const uint8_t* A, const uin
                                             int Nout, int F, int max_rows, int mean_rows, int ncu, float* partial,
                                             hipStream_t stream)
 {
+    const MxChoice c = choose(E, K, Nout, epi == MXEPI_SWIGLU, max_rows, mean_rows, partial != nullptr);
     const MxGemmArgs g = {A, As, gather, gather_rows, W, Ws, Hq, Hs, Y, offsets, E, K, Nw, Nout, F,
-                          max_rows, partial};
-    const long long narrow = (long long)std::min(E, max_rows) * std::max(1, (mean_rows + 63) / 64) * (Nout / 128);
-    if (epi != MXEPI_SWIGLU && E <= kMxMaxE<NarrowShape> && narrow_pays(mean_rows, narrow, K, ncu))
-        return launch_narrow<NarrowShape>(epi, g, ncu, stream);
-    const int tile_cols = epi == MXEPI_SWIGLU ? 128 : 256;
-    const long long ntn = (Nout + tile_cols - 1) / tile_cols, busy = std::min(E, max_rows);
-    if (mean_rows >= kLargeRows) {
-        auto most = [&](int bm) { return (busy == 1 ? (max_rows + bm - 1) / bm : max_rows / bm + busy) * ntn; };
-        if (most(MediumShape::BM) <= ncu)
-            return launch_epi<MediumShape>(epi, g, ncu, stream);
-        if (most(Shape128::BM) <= ncu && E <= kMxMaxE<Shape128>)
-            return launch_epi<Shape128>(epi, g, ncu, stream);
-        return launch_epi<LargeShape>(epi, g, ncu, stream);
-    }
-    const long long tiles = busy * ((mean_rows + 95) / 96 + (mean_rows == 0)) * ntn;
-    if (tiles < ncu)
-        return launch_epi<SmallShape>(epi, g, ncu, stream);
-    return launch_epi<MediumShape>(epi, g, ncu, stream);
+                          max_rows, c.split ? partial : nullptr};
+    return c.large ? launch_epi<LargeShape>(epi, g, ncu, stream) : launch_epi<PairShape>(epi, g, ncu, stream);
 }

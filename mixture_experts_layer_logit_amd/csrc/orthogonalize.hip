@@ -237,8 +237,8 @@ struct NsOp {
     }
 };
 
-typedef TileShape<256, 2, 4, 2, 4, 256, 1, 0> NsLarge;
-typedef TileShape<128, 2, 2, 2, 8, 128, 2, 0> NsSmall;
+typedef TileShape<256, 2, 4, 2, 4, 256, 1, false> NsLarge;
+typedef TileShape<128, 2, 2, 2, 8, 128, 2, false> NsSmall;
 
 // The tiles of a product: `full` of them in one piece, the others, fewer than blocks run
 // at a time, in `parts` parts along K, whose sums moe_ns_tail_kernel adds.

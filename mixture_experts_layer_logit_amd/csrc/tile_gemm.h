@@ -14,14 +14,13 @@ namespace moe {
 // Block tile BM x BN, WM x WN wavefronts, S stages.  The BN rows of W are two halves;
 // a wavefront takes the same rows of both, so that a gate and an up value of a hidden
 // column meet in one lane.  GM: m-tiles of a group that share W's columns (decode_tile).
-// UNIT: the operands have scales, 8 bytes for the 128 of a row and slice, which lie behind
-// the stages: those of two slices in two places in turn (2), or a slice's in a place for
-// each stage (1).
-template <int BM_, int WM_, int WN_, int S_, int GM_, int BN_, int PER_CU_, int UNIT_>
+// SCALES: the operands have scales, 8 bytes for the 128 of a row and slice, which lie behind
+// the stages, those of two slices in two places in turn.
+template <int BM_, int WM_, int WN_, int S_, int GM_, int BN_, int PER_CU_, bool SCALES_>
 struct TileShape {
     static constexpr int BM = BM_, BN = BN_, kHalf = BN / 2, kPerCu = PER_CU_;
     static constexpr int WM = WM_, WN = WN_, S = S_, GM = GM_, RB = 128;
-    static constexpr int kUnit = UNIT_;
+    static constexpr bool kScales = SCALES_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int kWavesPerSimd = kWaves / 4 * kPerCu;
     static constexpr int kWaveM = BM / WM, kWaveN = BN / WN;
@@ -29,18 +28,17 @@ struct TileShape {
     static constexpr int kHalfN = kWaveN / 2, kHalfF = kFN / 2;
     static constexpr int kRows = 1024 / RB;  // tile rows of a 1 KB load
     static constexpr int kLdsA = BM * RB, kLdsW = BN * RB;
-    // a load of scales takes 16 bytes (UNIT 2) or 4 a lane, of kSclRows rows of one operand
-    static constexpr int kSclRows = kUnit == 2 ? 64 : 32, kSclA = (BM + kSclRows - 1) / kSclRows * kSclRows;
-    static constexpr int kSclGroups = kUnit ? (kSclA + BN) / kSclRows : 0;
-    static constexpr int kBlkS = (kSclGroups + kWaves - 1) / kWaves;
-    static constexpr int kSclUnit = kSclGroups * kSclRows * 8 * kUnit, kSclUnits = kUnit == 1 ? S : 2;
-    static constexpr int kStage = kLdsA + kLdsW, kLds = S * kStage + kSclUnits * kSclUnit;
+    // a load of scales takes 16 bytes, two slices' of a row, a lane
+    static constexpr int kSclGroups = kScales ? (BM + BN) / 64 : 0, kBlkS = (kSclGroups + kWaves - 1) / kWaves;
+    static constexpr int kSclUnit = kSclGroups * 1024;
+    static constexpr int kStage = kLdsA + kLdsW, kLds = S * kStage + 2 * kSclUnit;
     static constexpr int kBlkA = BM / kRows / kWaves, kBlkW = BN / kRows / kWaves;  // loads per wavefront and stage
     static constexpr int kLoads = kBlkA + kBlkW;
     static constexpr int kTileFloats = BM * BN;
     static_assert(kFN % 2 == 0, "a wavefront takes rows of both halves of W");
     static_assert(kWaves % 4 == 0 && BM % (kRows * kWaves) == 0, "loads split evenly");
     static_assert(kBlkW % 2 == 0, "a load lies in one half of W");
+    static_assert(!kScales || (BM % 64 == 0 && BN % 64 == 0 && kSclGroups % kWaves == 0), "scale loads split evenly");
     static_assert(S >= 2 && (S - 1) * kLoads <= 63, "vmcnt range");
 };
 
@@ -49,19 +47,6 @@ struct TileShape {
 // consecutive rows touches every bank once.
 __device__ __forceinline__ int tile_swz(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ uint32_t tile_at(int row, int c) { return row * 128 + ((c ^ tile_swz(row)) << 4); }
-
-// One dword per lane from buffer `rsrc` at voff + soff into LDS at byte address
-// lds + 4 * lane (see dma16).
-__device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff)
-{
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
-    uint32_t so = __builtin_amdgcn_readfirstlane(soff);
-    __asm__("" : "+s"(so));
-    __asm__ volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                     :
-                     : "s"(m0), "v"(voff), "s"(rsrc), "s"(so)
-                     : "memory");
-}
 
 // dma16 for a wavefront whose lanes are all active, where `on` is all ones, or, where it is 0,
 // nothing: a condition without a branch, which would split a loop that is scheduled as a
@@ -78,7 +63,7 @@ __device__ __forceinline__ void dma16_if(uint32_t on, const i32x4& rsrc, uint32_
                      : "memory");
 }
 
-// The K loop over slices [k0, k1) (k0 a multiple of UNIT) (each 128 bytes of K) for a wavefront whose first L
+// The K loop over slices [k0, k1) (k0 even where there are scales) (each 128 bytes of K) for a wavefront whose first L
 // row fragments hold rows that count (the others are neither read nor multiplied).
 // issue(q, st, n0, n1) starts loads [n0, n1) of the kLoads of slice q into stage st,
 // W's first; scales(q, place, on) those of the scales from slice q on, if on; keep(q) is a mask that
@@ -102,12 +87,9 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
     const int lane = lane_id();
     const uint32_t rdA = tile_at(wm * S::kWaveM + (lane & 31), 4 * (lane >> 5));
     const uint32_t rdW = S::kLdsA + tile_at(wn * S::kHalfN + (lane & 31), 4 * (lane >> 5));
-    constexpr int kPitch = 8 * S::kUnit;  // bytes of a row's scales in a unit
-    const uint32_t scl = S::S * S::kStage + kPitch * (lane & 31) + 4 * (lane >> 5);
-    const uint32_t scA = scl + kPitch * wm * S::kWaveM, scW = scl + kPitch * (S::kSclA + wn * S::kHalfN);
-    auto scales_at = [&](int q, int stage) {  // where slice q's scales lie
-        return S::kUnit == 2 ? (q >> 1 & 1) * S::kSclUnit + (q & 1) * 8 : stage * S::kSclUnit;
-    };
+    const uint32_t scl = S::S * S::kStage + 16 * (lane & 31) + 4 * (lane >> 5);
+    const uint32_t scA = scl + 16 * wm * S::kWaveM, scW = scl + 16 * (S::BM + wn * S::kHalfN);
+    auto scales_at = [&](int q) { return (q >> 1 & 1) * S::kSclUnit + (q & 1) * 8; };  // where slice q's lie
     struct Frags {
         i32x4 w[2][S::kFN], a[2][S::kFM];
     };
@@ -125,18 +107,18 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
             nx.a[h][n - S::kFN] = v;
     };
     auto read_a_scale = [&](int i, uint32_t at) {
-        if constexpr (S::kUnit)
-            sa[i] = *reinterpret_cast<const int*>(lds + at + scA + i * 32 * kPitch);
+        if constexpr (S::kScales)
+            sa[i] = *reinterpret_cast<const int*>(lds + at + scA + i * 512);
     };
     auto read_w_scales = [&](uint32_t at) {
-        if constexpr (S::kUnit)
+        if constexpr (S::kScales)
 #pragma unroll
             for (int j = 0; j < S::kFN; ++j)
                 swn[j] = *reinterpret_cast<const int*>(lds + at + scW +
-                                                       kPitch * ((j / kHalfF) * S::kHalf + (j % kHalfF) * 32));
+                                                       16 * ((j / kHalfF) * S::kHalf + (j % kHalfF) * 32));
     };
     auto cut_scales = [&](int q) {
-        if constexpr (S::kUnit) {
+        if constexpr (S::kScales) {
             const int keep = loads.keep(q);
 #pragma unroll
             for (int i = 0; i < L; ++i)
@@ -151,15 +133,13 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
     // where LAST, the scales of slice q + 1 (at sc); where LOADS, the loads of slice q + S
     // into stage lst, and of scales.  A matrix instruction runs for 32 cycles, in which its wavefront can
     // issue the few instructions that follow it.
-    // In slice q's second k-step its own scales have been read by every wavefront, so their
-    // place is free once the slice's unit ends; what is loaded here is read S - 1 or more
-    // slices' loads later, behind a wait that leaves fewer than those in flight.  Behind the
-    // last slice it is not read at all.
-    auto next_scales = [&](int q, int stage) {
-        if constexpr (S::kUnit == 2)
+    // In the second k-step of an odd slice q its own scales, the last of their place, have
+    // been read by every wavefront: the place takes those of slices q + 3 and q + 4, which are
+    // read more than S - 1 slices' loads later, behind a wait that leaves fewer than those in
+    // flight.  Behind the last slice nothing is read.
+    auto next_scales = [&](int q) {
+        if constexpr (S::kScales)
             loads.scales(q + 3, (q + 3) >> 1 & 1, -(uint32_t)(q & 1));
-        if constexpr (S::kUnit == 1)
-            loads.scales(q + S::S, stage, ~0u);
     };
     constexpr int kEarly = S::kBlkW;  // loads issued in a slice's first k-step: W's
     constexpr int kFree = NM >= 16 ? 6 : NM > 2 ? NM / 2 : NM;     // instructions behind which its reads are spread
@@ -174,7 +154,7 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
             if (LOADS)
                 loads.issue(q + S::S, lst, LAST ? kEarly : 0, LAST ? S::kLoads : kEarly);
             if constexpr (LAST && LOADS)
-                next_scales(q, lst);
+                next_scales(q);
         }
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
@@ -193,7 +173,7 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
                     read_w_scales(sc);
                 if constexpr (LOADS)
                     if (m == 1)
-                        next_scales(q, lst);
+                        next_scales(q);
                 constexpr int kLate = S::kLoads - kEarly, kSafe = NM > 0 ? NM : 1;
                 if constexpr (LOADS)
                     loads.issue(q + S::S, lst, kEarly + m * kLate / kSafe, kEarly + (m + 1) * kLate / kSafe);
@@ -221,9 +201,9 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
             if (r / kPer == m)
                 read(r, f0, 0, 0);
         if (m >= NI && m % S::kFN == S::kFN - 1)
-            read_a_scale(m % kNI / S::kFN, scales_at(k0, 0));
+            read_a_scale(m % kNI / S::kFN, scales_at(k0));
         if (m == 0)
-            read_w_scales(scales_at(k0, 0));
+            read_w_scales(scales_at(k0));
         __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -240,7 +220,7 @@ __device__ __forceinline__ void tile_kloop(f32x16 (&acc)[S::kFM][S::kFN], const 
         // stricter)
         wait_vmcnt<LOADS ? (S::S - 2) * S::kLoads + kEarly : 0>();
         lds_barrier();
-        kstep(f1, f0, nxt * S::kStage, 0, scales_at(kt + 1, nxt), yes, more, kt, cur);
+        kstep(f1, f0, nxt * S::kStage, 0, scales_at(kt + 1), yes, more, kt, cur);
 #pragma unroll
         for (int j = 0; j < S::kFN; ++j)
             sw[j] = swn[j];
@@ -267,11 +247,10 @@ __device__ __forceinline__ void tile_product(f32x16 (&acc)[S::kFM][S::kFN], cons
 #pragma unroll
             for (int v = 0; v < 16; ++v)
                 acc[i][j][v] = 0.0f;
-    if constexpr (S::kUnit)
+    if constexpr (S::kScales)
 #pragma unroll
-        for (int u = 0; u < S::kSclUnits; ++u)
-            if (k0 + u * S::kUnit < k1)
-                loads.scales(k0 + u * S::kUnit, S::kUnit == 2 ? ((k0 >> 1) + u) & 1 : u, ~0u);
+        for (int u = 0; u < 2; ++u)
+            loads.scales(k0 + 2 * u, ((k0 >> 1) + u) & 1, k0 + 2 * u < k1 ? ~0u : 0u);
 #pragma unroll
     for (int q = 0; q < S::S; ++q)
         if (k0 + q < k1)
