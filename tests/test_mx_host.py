@@ -263,6 +263,9 @@ def test_bindings_as_a_process_first_call(fn, monkeypatch):
     for name in ("_f32", "_i32", "_bf16", "_codes"):
         monkeypatch.setattr(moe, name, None)
     monkeypatch.setattr(moe, "_packed", ())
+    monkeypatch.setattr(moe, "_device", None)
+    monkeypatch.setattr(moe, "_src_types", {})
+    monkeypatch.setattr(moe, "_scale_types", {})
     with pytest.raises(ValueError, match="GPU"):
         getattr(moe, fn)(**calls(torch)[fn], stream=0)
 
