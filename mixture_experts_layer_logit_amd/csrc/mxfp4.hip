@@ -261,8 +261,8 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
         const int lrow = S::kRows * wave + lane / 8;
         const int chunk = (lane % 8) ^ tile_swz(lrow);
         const uint32_t lchunk = (uint32_t)chunk * 16;
-        // the second half of a ragged slice reads behind the buffer: zeros
-        const uint32_t cutA = chunk >= 4 ? 0xf0000000u : 0;
+        // the missing half of a ragged slice reads behind the buffer: zeros
+        const uint32_t cutHalf = chunk >= 4 ? 0xf0000000u : 0;
         // first rows of the two halves of the weight tile; the second, or its end, may
         // lie behind the matrix
         const uint32_t half1 = EPI == MXEPI_SWIGLU ? (uint32_t)(g.F + t.n0) : (uint32_t)(t.n0 + S::kHalf);
@@ -319,7 +319,7 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
             const i32x4 &rsA, &rsW;
             const i32x4 (&rsS)[S::kBlkS];
             const uint32_t (&voffA)[S::kBlkA], (&voffS)[S::kBlkS];
-            uint32_t voffW, voffW1, row0, row1, step, lds0, cutA;
+            uint32_t voffW, voffW1, row0, row1, step, lds0, cutHalf;
             int keepS, wave, k0, k1, rot, last;
             __device__ __forceinline__ int slice_of(int q) const
             {
@@ -331,35 +331,36 @@ void moe_mxfp4_gemm_kernel(MxGemmArgs g)
             {
                 const uint32_t dst = lds0 + st * S::kStage + wave * 1024;
                 const int kb = slice_of(q);
-                const uint32_t soff = (uint32_t)kb * S::RB, cut = kb == last ? 0xffffffffu : 0;
+                const uint32_t soff = (uint32_t)kb * S::RB, cut = kb == last ? cutHalf : 0;
 #pragma unroll
                 for (int p = 0; p < S::kLoads; ++p) {
                     if (p < n0 || p >= n1)
                         continue;
                     if (p < S::kBlkW / 2)
-                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW, soff + row0 + p * step);
+                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, voffW | cut, soff + row0 + p * step);
                     else if (p < S::kBlkW)
-                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, EPI == MXEPI_SWIGLU ? voffW : voffW1,
+                        dma16(rsW, dst + S::kLdsA + S::kWaves * p * 1024, (EPI == MXEPI_SWIGLU ? voffW : voffW1) | cut,
                               soff + row1 + (p - S::kBlkW / 2) * step);
                     else
-                        dma16(rsA, dst + S::kWaves * (p - S::kBlkW) * 1024, voffA[p - S::kBlkW] | (cutA & cut), soff);
+                        dma16(rsA, dst + S::kWaves * (p - S::kBlkW) * 1024, voffA[p - S::kBlkW] | cut, soff);
                 }
             }
             __device__ __forceinline__ void scales(int q0, int place, uint32_t on) const
             {
                 const uint32_t dst = lds0 + S::S * S::kStage + place * S::kSclUnit;
-                const uint32_t soff = (uint32_t)slice_of(q0) * 8;
+                // in the lane's offset: what lies behind the operand's end reads as zeros
+                const uint32_t at = (uint32_t)slice_of(q0) * 8;
 #pragma unroll
                 for (int q = 0; q < S::kBlkS; ++q)
-                    dma16_if(on, rsS[q], dst + (wave + q * S::kWaves) * 1024, voffS[q], soff);
+                    dma16_if(on, rsS[q], dst + (wave + q * S::kWaves) * 1024, voffS[q] + at, 0);
             }
-            // the last slice's second half may be missing: its codes of A are zeros, and
-            // its scales, whatever lies there, must not be NaN.  (No row that is rotated
+            // the last slice's second half may be missing: its codes are zeros, and its
+            // scales, whatever lies there, must not be NaN.  (No row that is rotated
             // ends in half a slice: the last one stays the last.)
             __device__ __forceinline__ int keep(int q) const { return q == last ? keepS : -1; }
         };
         const Loads loads = {rsA,  rsW,  rsS,  voffA, voffS, voffW, voffW1, row0, row1, step, lds0,
-                             cutA, (lane >> 5) - 1, wave, k0, k1, rot, ragged};
+                             cutHalf, (lane >> 5) - 1, wave, k0, k1, rot, ragged};
 
         wait_vmcnt<0>();  // the previous tile's stores are out of the count
         __syncthreads();  // and every wave is done with its LDS

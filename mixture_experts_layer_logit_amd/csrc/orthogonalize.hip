@@ -658,8 +658,12 @@ __global__ __launch_bounds__(S::kThreads) void moe_ns_tail_kernel(NsArgs g, NsPl
 // else: three launches in place of 2 + 3 or more a step.  P grows to 3.44^steps where a
 // singular value is close to zero, and an error of A_0 with it: A_0 and P are held in fp64
 // (fp64 matrix cores; A_0's products of fp32 numbers are exact), and P X is an fp32
-// product.
+// product.  A singular value of zero stays one only as long as the
+// roundings of P, of 3.44^steps 2^-24, stay small (after 13 steps a gradient of rank 3 had
+// grown to 4e3), so longer runs take the tiles, whose X is rounded anew in every step and
+// cannot outgrow the iteration's range.
 constexpr int kFewRows = 64;
+constexpr int kFewSteps = 7;
 constexpr int kSlab = 64;         // columns of X at a time
 constexpr int kSlabPitch = 68;    // of a slab in LDS, [column][row]: neither operand order meets in few banks
 constexpr int kFewBytes = 1 << 19;  // partial sums of A_0 that one workgroup adds, at most
@@ -1027,11 +1031,12 @@ extern "C" size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols)
     NsArgs g = ns_args(count, rows, cols);
     if (count == 0)
         return 0;
-    if (g.m <= kFewRows) {
+    size_t few = 0;
+    if (g.m <= kFewRows) {  // the number of steps, which is not known here, decides
         NsFew w = few_plan(g);
-        return few_layout(w, g, nullptr);
+        few = few_layout(w, g, nullptr);
     }
-    return ns_layout(g, nullptr);
+    return std::max(few, ns_layout(g, nullptr));
 }
 
 // dtype 0 fp32, 1 bf16 gradients [count][rows][cols]; momentum (nullable) fp32; out bf16.
@@ -1044,7 +1049,7 @@ extern "C" hipError_t moe_launch_orthogonalize(int dtype, const void* grad, floa
     g.beta = beta, g.src_dtype = dtype, g.nesterov = nesterov;
     auto aligned = [](const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; };
     g.vec = cols % 4 == 0 && aligned(grad, dtype == 0 ? 16 : 8) && aligned(momentum, 16);
-    if (g.m <= kFewRows)
+    if (g.m <= kFewRows && steps <= kFewSteps)
         return launch_few(g, steps, (char*)ws, stream);
     ns_layout(g, (char*)ws);
     moe_ns_sums_kernel<<<dim3(g.parts, count), dim3(256), 0, stream>>>(g);
