@@ -405,7 +405,7 @@ __device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size
         ns_fetch<S, ONE>(lds, g.a + mat * g.m * g.mp, f0, i0, j0, g.m, g.mp);
     if constexpr (MODE == NS_UPDATE)
         ns_fetch<S, ONE>(lds, g.xt + ((size_t)st.src * g.count + mat) * g.n * g.mp, f0, i0, j0, g.n, g.mp);
-    // what the columns of this lane need: the diagonal of A or B there
+    // what the columns of this lane need: c dA + b, or the diagonal of B
     f32x4 dj[S::kFN][4];
     if constexpr (MODE != NS_GRAM) {
         const float* d = (MODE == NS_POLY ? g.da : g.db) + mat * g.mp;
@@ -415,6 +415,10 @@ __device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size
             for (int q = 0; q < 4; ++q) {
                 const int j = j0 + (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32 + 8 * q + 4 * (lane >> 5);
                 dj[fj][q] = *reinterpret_cast<const f32x4*>(d + min(j, g.mp - 4));
+                if constexpr (MODE == NS_POLY)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dj[fj][q][e] = fmaf(kNsC, dj[fj][q][e], kNsB);
             }
     }
     const float inv = 1.0f / g.sx;  // powers of two
@@ -449,6 +453,7 @@ __device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size
             const int c0 = (fj / S::kHalfF) * S::kHalf + wn * S::kHalfN + (fj % S::kHalfF) * 32;
             if (!held_i || j0 + c0 >= g.mp)
                 continue;
+            const bool diagonal = MODE != NS_UPDATE && ib == j0 + c0;  // runs through this fragment
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = c0 + 8 * q + 4 * (lane >> 5), j = j0 + c;
@@ -457,24 +462,32 @@ __device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size
                 f16x4* at = reinterpret_cast<f16x4*>(lds + ns_staged<S>(sr, c));
                 f16x4 o;
                 if constexpr (MODE == NS_GRAM) {
+                    o = __builtin_convertvector(v * (inv * inv * kNsScale), f16x4);
+                    if (diagonal)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float s = v[e] * (inv * inv);
-                        if (j + e == i && i < g.m)
-                            g.da[mat * g.mp + i] = s;
-                        o[e] = (_Float16)(j + e == i ? 0.0f : s * kNsScale);
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e == i) {
+                                if (i < g.m)
+                                    g.da[mat * g.mp + i] = v[e] * (inv * inv);
+                                o[e] = (_Float16)0.0f;
+                            }
                 } else if constexpr (MODE == NS_POLY) {
+                    // c (A A)_ij with A = O + diag: the square of O, and twice O's entry
                     const f16x4 a = *at;
+                    f32x4 b;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float off = (float)a[e] * (1.0f / kNsScale);
-                        const float sq = v[e] * (1.0f / (kNsScale * kNsScale));
-                        if (j + e == i && i < g.m)
-                            g.db[mat * g.mp + i] = fmaf(kNsC, fmaf(di, di, sq), kNsB * di);
-                        const float b = fmaf(kNsC, fmaf(di + dj[fj][q][e], off, sq), kNsB * off);
-                        o[e] = (_Float16)(j + e == i ? 0.0f : b * kNsScale);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        b[e] = fmaf(fmaf(kNsC, di, dj[fj][q][e]), (float)a[e], v[e] * (kNsC / kNsScale));
+                    o = __builtin_convertvector(b, f16x4);
+                    if (diagonal)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e == i) {
+                                if (i < g.m)
+                                    g.db[mat * g.mp + i] =
+                                        fmaf(kNsC, fmaf(di, di, v[e] * (1.0f / (kNsScale * kNsScale))), kNsB * di);
+                                o[e] = (_Float16)0.0f;
+                            }
                 } else {
                     const f16x4 hi = *at;
                     f32x4 y;
@@ -488,11 +501,8 @@ __device__ __forceinline__ void ns_store(const NsArgs& g, const NsStep& st, size
                         o = __builtin_bit_cast(f16x4, __builtin_convertvector(y * inv, bf16x4));
                     } else {
                         f16x4 l;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[e] = (_Float16)y[e];
-                            l[e] = (_Float16)((y[e] - (float)o[e]) * kNsLow);
-                        }
+                        o = __builtin_convertvector(y, f16x4);
+                        l = __builtin_convertvector((y - __builtin_convertvector(o, f32x4)) * kNsLow, f16x4);
                         *reinterpret_cast<f16x4*>(g.low + ns_frag(g, mat, ib / 32, (j0 + c0) / 32) + q * 256 + lane * 4) = l;
                     }
                 }
