@@ -564,8 +564,8 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  *   out [count][rows][cols] = X, rounded to bf16 once
  * G is fp32 (as moe_backward writes it) or bf16 (grad_dtype).  |U|_F is summed in
  * fp64, in a fixed order.  The products run on fp16 operands with fp32 sums,
- * scaled so that no range is lost: out is within about 1.5e-3 of the 64-bit result
- * in the norm before its rounding.  The same bits on every run.  A matrix whose U
+ * scaled so that no range is lost: before its rounding out is within about 1.5e-3 of
+ * the 64-bit result in the norm (3e-3 for matrices of rank one).  The same bits on every run.  A matrix whose U
  * holds a NaN or an infinity becomes NaN as a whole and leaves the others alone.
  * 1 <= rows, cols <= 65536 (any size, no alignment beyond an element's), rows *
  * cols < 2^30, 0 <= count <= 32768, 1 <= steps <= 64 (5 is usual).  Needs ws_bytes
