@@ -572,3 +572,73 @@ def test_training_step_then_serving():
         t, j = np.nonzero(i["topk_idx"] == e)
         np.add.at(full, t, i["topk_w"][t, j][:, None] * v[i["slot"][t, j] - rows[0]])
     assert np.linalg.norm(y - full) <= 0.34 * np.linalg.norm(full)
+
+
+# ---------------------------------------------------------------- offsets that pass 32 bits
+def big_ints(n):
+    return torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda", generator=torch.Generator("cuda").manual_seed(n % 1000))
+
+
+@pytest.fixture
+def roomy():
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_quantise_more_than_2_32_values(roomy):
+    """Rows behind the first 2^32 values get what they get by themselves."""
+    K, rows = 4096, (1 << 20) + 77
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_()
+    q = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(rows, K // BLK, dtype=torch.uint8, device="cuda")
+    moe.moe_quantize_mxfp4(x, q, s)
+    for at in (0, 1 << 19, rows - 100):
+        tq, ts = torch.empty_like(q[:100]), torch.empty_like(s[:100])
+        moe.moe_quantize_mxfp4(x[at:at + 100], tq, ts)
+        assert torch.equal(tq, q[at:at + 100]) and torch.equal(ts, s[at:at + 100]), at
+    moe.moe_dequantize_mxfp4(q, s, x)
+    for at in (0, 1 << 19, rows - 100):
+        back = torch.empty(100, K, dtype=torch.bfloat16, device="cuda")
+        moe.moe_dequantize_mxfp4(q[at:at + 100], s[at:at + 100], back)
+        assert torch.equal(back, x[at:at + 100]), at
+
+
+def test_weights_of_more_than_4_gib(roomy):
+    """Both layers' last expert lies behind the first 4 GiB of codes; 64 of each layer's
+    columns, from all over, against 64-bit products."""
+    T, d, F, E = 9, 16384, 8192, 65
+    g = gen(65)
+    off = dev(np.array([0, 4] + [4] * (E - 2) + [T], np.int32))  # the first and the last
+    xq, xs, x = quantised(g.standard_normal((T, d)))
+    hq, hs, h = quantised(np.maximum(g.standard_normal((T, F)), -0.5))
+    src = dev(np.arange(T, dtype=np.int32))
+    cols = np.sort(g.choice(F // BLK, 2, replace=False))
+    hidden = np.concatenate([np.arange(c * BLK, (c + 1) * BLK) for c in cols])
+    rows_of = dict(up=np.concatenate([hidden, F + hidden]), down=np.sort(g.choice(d, 64, replace=False)))
+    W, sc = {}, {}
+    for name, n, K in (("up", 2 * F, d), ("down", d, F)):
+        W[name] = big_ints(E * n * K // 2).view(E, n, K // 2)
+        sc[name] = (big_ints(E * n * K // BLK).view(E, n, K // BLK) % 5) + 118
+    assert min(W["up"].numel(), W["down"].numel()) > 1 << 32
+
+    def picked(name, e):
+        at = torch.from_numpy(rows_of[name]).cuda()
+        q, s = W[name][e].index_select(0, at).cpu().numpy(), sc[name][e].index_select(0, at).cpu().numpy()
+        return ref.widen(q, s.astype(np.int64) - 127)
+
+    p = moe.problem(T, d, E, 1, F, act="swiglu")
+    ws = torch.empty(moe.moe_mxfp4_workspace_size(p), dtype=torch.uint8, device="cuda")
+    oq = torch.zeros(T, F // 2, dtype=torch.uint8, device="cuda")
+    os_ = torch.zeros(T, F // BLK, dtype=torch.uint8, device="cuda")
+    y = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_up_mxfp4(p, dev(xq), dev(xs), src, off, W["up"], sc["up"], oq, os_, ws=ws)
+    moe.moe_expert_down_mxfp4(p, dev(hq), dev(hs), off, W["down"], sc["down"], y, ws=ws)
+    torch.cuda.synchronize()
+    for e, r in ((0, slice(0, 4)), (E - 1, slice(4, T))):
+        v, dv = ref.hidden(x[r], picked("up", e), "swiglu", 2 * BLK)
+        codes = oq[r].cpu().numpy().reshape(-1, F // BLK, BLK // 2)[:, cols].reshape(-1, BLK)
+        ref.check_quantised(codes, os_[r].cpu().numpy()[:, cols].astype(np.int64) - 127, v, dv, f"up, expert {e}")
+        v, dv = ref.product(h[r], picked("down", e))
+        over = np.abs(y[r].double().cpu().numpy()[:, rows_of["down"]] - v) - (dv + ref.U8 * (np.abs(v) + dv))
+        assert np.all(over <= 0), f"down, expert {e}"

@@ -264,3 +264,21 @@ def test_two_streams_at_once():
             moe.moe_orthogonalize(g, out, ws=ws, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.parametrize("shape", [(40, 65536, 1024), (5000, 8, 65536)], ids=lambda s: "-".join(map(str, s)))
+def test_more_than_2_31_values(shape):
+    """The first and the last matrix get what they get by themselves.  Their plans differ by
+    the number of matrices, so both are within 1.5e-3 of the same 64-bit result in the norm
+    and then within bf16's half step U8: 2 (1.5e-3 + U8) of each other."""
+    torch.cuda.empty_cache()
+    print(f"[orthogonalize] {shape}", flush=True)
+    g = torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    assert g.numel() > 1 << 31
+    out = run(g)
+    for i in (0, shape[0] - 1):
+        one = run(g[i]).double()
+        assert torch.linalg.norm(out[i].double() - one) <= 2 * (1.5e-3 + ref.U8) * torch.linalg.norm(one), i
+        assert 0.6 < torch.linalg.norm(one) / min(shape[1:]) ** 0.5 < 1.3  # singular values around 1
+    del g, out, one
+    torch.cuda.empty_cache()
