@@ -563,10 +563,23 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  *   the fewer rows:  A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A^2) X
  *   out [count][rows][cols] = X, rounded to bf16 once
  * G is fp32 (as moe_backward writes it) or bf16 (grad_dtype).  |U|_F is summed in
- * fp64, in a fixed order.  The products run on fp16 operands with fp32 sums,
- * scaled so that no range is lost: before its rounding out is within about 1.5e-3 of
- * the 64-bit result in the norm (3e-3 for matrices of rank one).  The same bits on every run.  A matrix whose U
+ * fp64, in a fixed order.  The same bits on every run.  A matrix whose U
  * holds a NaN or an infinity becomes NaN as a whole and leaves the others alone.
+ * Error against the 64-bit result, in the norm of that result, before out's own
+ * rounding.  Up to 64 rows (or columns) and 7 steps: fp64 steps and one fp32 product, at
+ * most 1e-4 up to 5 steps and 1e-3 at 7.  Else the products run on fp16 operands
+ * with fp32 sums, scaled so that no range is lost.  The quintic's slope, up to 3.97,
+ * carries each step's roundings on through the next, so the error goes by the matrix and the
+ * steps and has no bound that serves them all.  The largest seen:
+ *   steps                                                      1-5      6-8      9-64
+ *   full rank, singular values that differ (Gaussian
+ *   gradients, sums over more tokens than rows)                1.5e-3   4e-3     2e-2
+ *   equal singular values: orthonormal or repeated rows,
+ *   blocks of equal entries                                    1.2e-2   3e-2     0.12
+ *   singular values of zero (fewer tokens than rows)           1.5e-3   2.5e-3   -
+ * What a rounding leaves in the direction of a singular value next to zero grows by 3.44 a
+ * step, in this as in any arithmetic: here it is 2e-2 of the result at 10 steps and 0.2 at
+ * 12, and behind those these directions are as large as the rest.
  * 1 <= rows, cols <= 65536 (any size, no alignment beyond an element's), rows *
  * cols < 2^30, 0 <= count <= 32768, 1 <= steps <= 64 (5 is usual).  Needs ws_bytes
  * >= moe_orthogonalize_workspace_size (16-byte aligned). */

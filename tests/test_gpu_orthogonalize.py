@@ -282,3 +282,74 @@ def test_more_than_2_31_values(shape):
         assert 0.6 < torch.linalg.norm(one) / min(shape[1:]) ** 0.5 < 1.3  # singular values around 1
     del g, out, one
     torch.cuda.empty_cache()
+
+
+def structured(kind):
+    """Matrices of one kind of singular values, each next to no tile's size."""
+    g = gen(31)
+    if kind == "gaussian":
+        return g.standard_normal((200, 300))
+    if kind == "tokens":
+        return gradients(g, 1, 300, 200, "full")[0]
+    if kind == "orthonormal":
+        return np.eye(300, 1000)
+    if kind == "noisy orthonormal":
+        return np.eye(300, 1000) + 0.01 * g.standard_normal((300, 1000)) / np.sqrt(1000)
+    if kind.startswith("blocks"):  # of ones along the diagonal
+        b, rows, cols = {"blocks 4": (4, 130, 1001), "blocks 4 long": (4, 300, 2000), "blocks 4 small": (4, 100, 140),
+                         "blocks 13": (13, 130, 400)}[kind]
+        u = np.zeros((rows, cols))
+        for i in range(b):
+            u[i * rows // b:(i + 1) * rows // b, i * cols // b:(i + 1) * cols // b] = 1
+        return u
+    if kind == "block constant":
+        return np.kron(np.array([[1.0, 2.0], [3.0, 1.0]]), np.ones((128, 128)))
+    if kind == "repeated rows":
+        return g.standard_normal((22, 300))[g.integers(0, 22, 100)]
+    return gradients(g, 1, 200, 300, "rank3")[0] if kind == "rank 3" else np.outer(g.standard_normal(200), g.standard_normal(300))
+
+
+# The figures of include/moe.h: the error before out's rounding, in the norm of the result,
+# up to 5, 8 and 64 steps
+DIFFER, EQUAL, ZEROS = (1.5e-3, 4e-3, 2e-2), (1.2e-2, 3e-2, 0.12), (1.5e-3, 2.5e-3, None)
+
+
+@pytest.mark.parametrize("kind,steps,figures", [
+    ("gaussian", (3, 5, 8, 14, 20, 40), DIFFER), ("tokens", (3, 5, 8, 20, 40), DIFFER), ("orthonormal", (5, 8, 20, 40), EQUAL),
+    ("noisy orthonormal", (5, 8, 20, 40), EQUAL), ("blocks 4", (3, 5, 8, 12), EQUAL), ("blocks 4 long", (5, 8), EQUAL),
+    ("blocks 4 small", (5, 8), EQUAL), ("blocks 13", (5, 8), EQUAL), ("block constant", (5, 8), EQUAL), ("repeated rows", (5, 8), EQUAL),
+    ("rank 3", (5, 7, 8), ZEROS), ("rank 1", (5, 7, 8), ZEROS)], ids=lambda v: v.replace(" ", "_") if isinstance(v, str) else "")
+def test_the_error_as_documented(kind, steps, figures):
+    """Within the documented figure of the 64-bit result in the norm; then rounded to bf16. Where
+    the values are all different, the rounding is as that of the 64-bit result, r, and independent
+    of the error: their squares add up, over 6e4 values with a deviation of r^2 / 270 from the
+    roundings and of about that from the product of both, ten of them. Equal values are rounded
+    the same way, each by U8 at most."""
+    u = structured(kind).astype(np.float32)
+    for n in steps:
+        print(f"[orthogonalize] {kind} {n}", flush=True)
+        out = run(dev(u), steps=n).double().cpu().numpy()
+        want = ref.orthogonal_by_products(u.astype(np.float64), n)
+        figure = figures[0 if n <= 5 else 1 if n <= 8 else 2]
+        size, off = np.linalg.norm(want), np.linalg.norm(out - want)
+        if figures is EQUAL:
+            assert off <= (figure * (1 + ref.U8) + ref.U8) * size, n
+        else:
+            r = np.linalg.norm(torch.from_numpy(want).to(torch.bfloat16).double().numpy() - want)
+            assert off ** 2 <= (figure * size) ** 2 + 1.04 * r ** 2, n
+
+
+@pytest.mark.parametrize("kind", ["rank 1", "rank 3", "orthonormal", "ones", "halves"])
+@pytest.mark.parametrize("steps,figure", [(5, 1e-4), (7, 1e-3)])
+def test_the_error_of_few_rows_as_documented(kind, steps, figure):
+    """Up to 64 rows: an element's error beyond bf16's half step is the documented one's."""
+    g = gen(32)
+    for m, n in ((8, 4096), (64, 64), (1000, 64), (33, 500)):
+        u = {"rank 1": lambda: np.outer(g.standard_normal(m), g.standard_normal(n)), "rank 3": lambda: gradients(g, 1, m, n, "rank3")[0],
+             "orthonormal": lambda: np.eye(m, n), "ones": lambda: np.ones((m, n)),
+             "halves": lambda: np.kron(np.array([[1.0, 2.0], [3.0, 1.0]]), np.ones((m, n)))[m // 2:m // 2 + m, n // 2:n // 2 + n]}[kind]()
+        u = u.astype(np.float32)
+        out = run(dev(u), steps=steps).double().cpu().numpy()
+        want = ref.orthogonal_by_products(u.astype(np.float64), steps)
+        beyond = np.maximum(np.abs(out - want) - ref.U8 * np.abs(want), 0)
+        assert np.linalg.norm(beyond) <= figure * (1 + ref.U8) * np.linalg.norm(want), (m, n)
