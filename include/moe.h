@@ -582,7 +582,10 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  * 12, and behind those these directions are as large as the rest.
  * 1 <= rows, cols <= 65536 (any size, no alignment beyond an element's), rows *
  * cols < 2^30, 0 <= count <= 32768, 1 <= steps <= 64 (5 is usual).  Needs ws_bytes
- * >= moe_orthogonalize_workspace_size (16-byte aligned). */
+ * >= moe_orthogonalize_workspace_size (16-byte aligned), which suffices for any number of
+ * steps: 10 to 12 bytes a value of the matrices padded to 64 rows and columns, and at most
+ * 64 MiB; up to 64 rows (or columns) never more than 1.1 GiB, or 36 KB a matrix
+ * where that is more, since longer runs of larger batches are taken in parts. */
 moe_status moe_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t cols, size_t* bytes);
 moe_status moe_orthogonalize(const void* grad, int32_t grad_dtype, float* momentum, float beta, int32_t nesterov,
                              int32_t count, int32_t rows, int32_t cols, int32_t steps, void* out, void* ws,

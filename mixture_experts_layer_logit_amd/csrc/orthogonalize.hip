@@ -697,7 +697,7 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 struct NsFew {
     double* partial;  // [count][chunks][mt (mt + 1) / 2][256] partial A_0, tiles on and below the diagonal
-    float* p;         // [count][64][64] P
+    float* p;         // [count][16 mt][16 mt] P
     double* inv;      // [count] 1 / |U|
     int mt, chunks;   // 16-row tiles, workgroups a matrix in the first pass
 };
@@ -856,7 +856,7 @@ __global__ __launch_bounds__(640) void moe_ns_few_steps_kernel(NsArgs g, NsFew w
         __syncthreads();
     }
     for (int q = threadIdx.x; q < M * M; q += blockDim.x)
-        w.p[(mat * kFewRows + q / M) * kFewRows + q % M] = (float)P[q / M][q % M];
+        w.p[mat * M * M + q] = (float)P[q / M][q % M];
 #endif
 }
 
@@ -869,7 +869,7 @@ __global__ __launch_bounds__(256) void moe_ns_few_apply_kernel(NsArgs g, NsFew w
     const int lane = lane_id(), wave = threadIdx.x / kWave, M = 16 * w.mt;
     const size_t mat = blockIdx.y, base = mat * g.rows * g.cols;
     for (int q = threadIdx.x; q < M * M; q += 256)
-        P[q / M * kSlabPitch + q % M] = w.p[(mat * kFewRows + q / M) * kFewRows + q % M];
+        P[q / M * kSlabPitch + q % M] = w.p[mat * M * M + q];
     const double inv = w.inv[mat];
     const bool tall = g.rows > g.cols;
     for (int k0 = blockIdx.x * kSlab; k0 < g.n; k0 += gridDim.x * kSlab) {
@@ -904,6 +904,7 @@ using namespace moe;
 constexpr int kNsCus = 256;      // of gfx950
 constexpr int kNsMaxParts = 16;  // K parts of a split tile
 constexpr int kNsMinPart = 4;    // slices of a part
+constexpr size_t kTilePart = size_t(1) << 30;  // bytes of the matrices of few rows that take the tiles at a time
 
 size_t ns_round(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -967,7 +968,7 @@ NsFew few_plan(const NsArgs& g)
 size_t few_layout(NsFew& w, const NsArgs& g, char* ws)
 {
     const size_t c = g.count, partial = ns_round(8 * c * w.chunks * (w.mt * (w.mt + 1) / 2) * 256);
-    const size_t p = ns_round(4 * c * kFewRows * kFewRows);
+    const size_t p = ns_round(4 * c * 256 * w.mt * w.mt);
     w.partial = (double*)ws;
     w.p = (float*)(ws + partial);
     w.inv = (double*)(ws + partial + p);
@@ -986,8 +987,8 @@ hipError_t launch_few(const NsArgs& g, int steps, char* ws, hipStream_t stream)
     return hipGetLastError();
 }
 
-// The workspace's pieces; returns its size.
-size_t ns_layout(NsArgs& g, char* ws)
+// The pieces of the workspace that grow with the number of matrices; returns their size.
+size_t ns_pieces(NsArgs& g, char* ws)
 {
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -1004,14 +1005,55 @@ size_t ns_layout(NsArgs& g, char* ws)
     g.da = (float*)take(4 * c * g.mp);
     g.db = (float*)take(4 * c * g.mp);
     g.sums = (double*)take(8 * c * kNsSums);
+    return off;
+}
+
+// All of the tiles' workspace; returns its size.
+size_t ns_layout(NsArgs& g, char* ws)
+{
+    const size_t off = ns_pieces(g, ws);
     size_t partial = 0;
     for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE}) {
         NsPlan p;
         const int floats = ns_large(g, mode, p) ? NsLarge::kTileFloats : NsSmall::kTileFloats;
         partial = std::max(partial, (size_t)p.tail * p.parts * floats * 4);
     }
-    g.partial = (float*)take(partial);
-    return off;
+    g.partial = (float*)(ws + off);
+    return off + ns_round(partial);
+}
+
+// Matrices that take the tiles at a time.  Up to 64 rows only runs of more than kFewSteps
+// steps take them, on rows padded to 64, with up to a thousand times the bytes of the
+// three kernels that the usual steps take.  The workspace, whose size does not know the
+// steps, holds a part of such a batch: kTilePart bytes, or one matrix.  Eight steps in
+// ms, the batch at once / in parts of 1 GiB / of 512 / of 256 MiB:
+//   200 of 8 x 65536 (5.0 GB at once)    17.6 / 18.5 / 21.1 / 21.4
+//   100 of 32 x 65536 (2.8 GB)            9.5 / 10.4 / 11.8 / 12.9
+//   200 of 64 x 16384 (1.6 GB)            5.7 /  5.8 /  6.5 /  6.6
+//   32768 of 32 x 32 (1.0 GB)             8.7 /  8.8 /  8.7 /  8.1
+int tile_batch(const NsArgs& g)
+{
+    if (g.m > kFewRows || g.count == 0)
+        return g.count;
+    NsArgs one = g;
+    one.count = 1;
+    const size_t most = std::max<size_t>(1, kTilePart / ns_pieces(one, nullptr));
+    const int parts = (int)((g.count + most - 1) / most);
+    return (g.count + parts - 1) / parts;
+}
+
+// Bytes of the tiles' workspace: of a whole part of the batch, and of what is left.
+size_t tile_bytes(NsArgs g)
+{
+    const int count = g.count;
+    g.count = tile_batch(g);
+    const int rest = count % g.count;
+    size_t bytes = ns_layout(g, nullptr);
+    if (rest) {
+        g.count = rest;
+        bytes = std::max(bytes, ns_layout(g, nullptr));
+    }
+    return bytes;
 }
 
 NsArgs ns_args(int count, int rows, int cols)
@@ -1049,6 +1091,24 @@ void launch_product(const NsArgs& g, const NsChoice& c, const NsStep& st, hipStr
 {
     c.large ? launch_shape<NsLarge, MODE>(g, c.plan, st, stream) : launch_shape<NsSmall, MODE>(g, c.plan, st, stream);
 }
+
+// Momentum and start, and the steps' products.
+void launch_tiles(NsArgs& g, int steps, char* ws, hipStream_t stream)
+{
+    ns_layout(g, ws);
+    moe_ns_sums_kernel<<<dim3(g.parts, g.count), dim3(256), 0, stream>>>(g);
+    moe_ns_init_kernel<<<dim3(g.mp / 64 * (g.np / 64), g.count), dim3(256), 0, stream>>>(g);
+    NsChoice c[3];
+    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE})
+        c[mode].large = ns_large(g, mode, c[mode].plan);
+    const bool wide = g.cols % 8 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
+    for (int s = 0; s < steps; ++s) {
+        const NsStep st = {s & 1, s >= steps - 2, s == steps - 1, wide};
+        launch_product<NS_GRAM>(g, c[NS_GRAM], st, stream);
+        launch_product<NS_POLY>(g, c[NS_POLY], st, stream);
+        launch_product<NS_UPDATE>(g, c[NS_UPDATE], st, stream);
+    }
+}
 }  // namespace
 
 extern "C" size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols)
@@ -1061,7 +1121,7 @@ extern "C" size_t moe_orthogonalize_scratch_bytes(int count, int rows, int cols)
         NsFew w = few_plan(g);
         few = few_layout(w, g, nullptr);
     }
-    return std::max(few, ns_layout(g, nullptr));
+    return std::max(few, tile_bytes(g));
 }
 
 // dtype 0 fp32, 1 bf16 gradients [count][rows][cols]; momentum (nullable) fp32; out bf16.
@@ -1076,17 +1136,14 @@ extern "C" hipError_t moe_launch_orthogonalize(int dtype, const void* grad, floa
     g.vec = cols % 4 == 0 && aligned(grad, dtype == 0 ? 16 : 8) && aligned(momentum, 16);
     if (g.m <= kFewRows && steps <= kFewSteps)
         return launch_few(g, steps, (char*)ws, stream);
-    ns_layout(g, (char*)ws);
-    moe_ns_sums_kernel<<<dim3(g.parts, count), dim3(256), 0, stream>>>(g);
-    moe_ns_init_kernel<<<dim3(g.mp / 64 * (g.np / 64), count), dim3(256), 0, stream>>>(g);
-    NsChoice c[3];
-    for (int mode : {NS_GRAM, NS_POLY, NS_UPDATE})
-        c[mode].large = ns_large(g, mode, c[mode].plan);
-    for (int s = 0; s < steps; ++s) {
-        const NsStep st = {s & 1, s >= steps - 2, s == steps - 1, cols % 8 == 0 && aligned(out, 16)};
-        launch_product<NS_GRAM>(g, c[NS_GRAM], st, stream);
-        launch_product<NS_POLY>(g, c[NS_POLY], st, stream);
-        launch_product<NS_UPDATE>(g, c[NS_UPDATE], st, stream);
+    const size_t each = (size_t)rows * cols;
+    for (int first = 0, part = tile_batch(g); first < count; first += part) {
+        NsArgs p = g;
+        p.count = std::min(part, count - first);
+        p.grad = (const char*)grad + first * each * (dtype == 0 ? 4 : 2);
+        p.momentum = momentum ? momentum + first * each : nullptr;
+        p.out = g.out + first * each;
+        launch_tiles(p, steps, (char*)ws, stream);
     }
     return hipGetLastError();
 }

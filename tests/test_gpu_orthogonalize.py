@@ -353,3 +353,34 @@ def test_the_error_of_few_rows_as_documented(kind, steps, figure):
         want = ref.orthogonal_by_products(u.astype(np.float64), steps)
         beyond = np.maximum(np.abs(out - want) - ref.U8 * np.abs(want), 0)
         assert np.linalg.norm(beyond) <= figure * (1 + ref.U8) * np.linalg.norm(want), (m, n)
+
+
+@pytest.mark.parametrize("shape,dtype,nesterov", [((47, 8, 65536), "f32", True), ((47, 65533, 8), "bf16", False), ((599, 40, 9000), "bf16", True),
+                                                  ((1501, 64, 2049), "f32", None)], ids=lambda v: "-".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_long_runs_of_few_rows_in_parts(shape, dtype, nesterov):
+    """More than 7 steps of matrices of up to 64 rows are taken in parts of the batch: those on
+    both sides of every border, the momentum of all, and nothing behind the last."""
+    print(f"[orthogonalize] {shape} {dtype} {nesterov}", flush=True)
+    m, n = min(shape[1:]), max(shape[1:])
+    pad = lambda v: -(-v // 64) * 64
+    each = 2 * m * pad(n) + 4 * n * 64 + 2 * pad(n) * 64 + 4 * m * 64  # bytes, and a little
+    part = -(-shape[0] // -(-shape[0] // ((1 << 30) // each)))
+    assert 1 < part < shape[0]
+    rng = torch.Generator("cuda").manual_seed(14)
+    g = torch.randn(shape, device="cuda", generator=rng) * torch.exp(torch.randn(*shape[:2], 1, device="cuda", generator=rng))
+    g = g.to(torch.bfloat16) if dtype == "bf16" else g
+    mom = None if nesterov is None else 8 * torch.randn(shape, device="cuda", generator=rng)
+    old = None if mom is None else mom.double()
+    out = torch.full((shape[0] + 1, *shape[1:]), 9.0, dtype=torch.bfloat16, device="cuda")
+    size = moe.moe_orthogonalize_workspace_size(*shape)
+    ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    moe.moe_orthogonalize(g, out[:-1], momentum=mom, beta=0.9, nesterov=bool(nesterov), steps=8, ws=ws[:size])
+    torch.cuda.synchronize()
+    assert torch.all(out[-1] == 9.0) and torch.all(ws[size:] == 0xFF)
+    u, beta = g.double(), float(np.float32(0.9))
+    if mom is not None:
+        want = beta * old + u
+        assert torch.all((mom.double() - want).abs() <= ref.U24 * want.abs() * 1.001)
+        u = u + beta * mom.double() if nesterov else mom.double()
+    for i in sorted({0, part - 1, part, 2 * part - 1, 2 * part, shape[0] - 1} & set(range(shape[0]))):
+        check(out[i].double().cpu().numpy(), u[i].cpu().numpy(), 8, f"matrix {i} of parts of {part}")

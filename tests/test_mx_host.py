@@ -295,3 +295,16 @@ def test_reference_update_error_goes_by_the_matrix_and_the_steps():
     assert error(normal, 5) <= 1.5e-3 < error(normal, 14) <= 2e-2
     assert 1.5e-3 < error(np.eye(300, 1000), 5) <= 1.2e-2
     assert 3e-3 < error(equal, 5) <= 1.2e-2 and error(equal, 8) <= 3e-2
+
+
+@pytest.mark.parametrize("count,rows,cols", [(5000, 8, 65536), (2000, 65536, 16), (32768, 8, 16), (8192, 64, 1024), (1500, 33, 4096)])
+def test_orthogonalize_workspace_of_few_rows_stays_small(count, rows, cols):
+    """Up to 64 rows the usual steps read the gradient twice and keep sums of its small side,
+    no copies of the batch; those of longer runs are taken in parts of 1 GiB, with at most
+    64 MiB of partial tiles."""
+    n = moe.moe_orthogonalize_workspace_size(count, rows, cols)
+    mt = -(-min(rows, cols) // 16)  # tiles of 16: fp64 on and below the diagonal, fp32 all of them
+    small = count * (mt * (mt + 1) // 2 * 2048 + mt * mt * 1024 + 8) + (1 << 20)
+    assert n <= max(1088 << 20, small), f"{n / 2 ** 20:.0f} MiB"
+    # a single matrix of such rows fits as ever
+    assert moe.moe_orthogonalize_workspace_size(1, rows, cols) <= 320 << 20
