@@ -701,8 +701,8 @@ def moe_orthogonalize_workspace_size(count, rows, cols) -> int:
 
 def moe_orthogonalize(grad, out, momentum=None, beta=0.95, nesterov=True, steps=5, ws=None, stream=None):
     """The orthogonalised update of each matrix of grad (fp32 or bf16, [count, rows,
-    cols] or [rows, cols]) into out (bf16).  momentum (fp32, updated): M <- beta M + G,
-    of which the update is G + beta M (nesterov) or M; None: it is G, beta and
+    cols] or [rows, cols]) into out (bf16, of that shape).  momentum (fp32, of that shape,
+    updated): M <- beta M + G, of which the update is G + beta M (nesterov) or M; None: it is G, beta and
     nesterov do not count."""
     if _f32 is None:
         _fill_types()
@@ -714,6 +714,9 @@ def moe_orthogonalize(grad, out, momentum=None, beta=0.95, nesterov=True, steps=
     rows, cols = grad.shape[-2:]
     count, n = (grad.shape[0] if grad.dim() == 3 else 1), grad.numel()
     _refuse((("out", out, _bf16), ("momentum", momentum, _f32)), (("out", out, n), ("momentum", momentum, n)))
+    for name, t in (("out", out), ("momentum", momentum)):
+        if t is not None and not isinstance(t, int) and (t.shape[-2:] != grad.shape[-2:] or t.numel() != n):
+            raise ValueError(f"{name} is {tuple(t.shape)}, grad {tuple(grad.shape)}")
     _on_gpu(stream, (grad, out, momentum, ws))
     _check(load().moe_orthogonalize(_ptr(grad), dt, _ptr(momentum), float(beta),
                                     int(bool(nesterov) and momentum is not None), count, rows, cols, int(steps),

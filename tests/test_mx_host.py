@@ -308,3 +308,21 @@ def test_orthogonalize_workspace_of_few_rows_stays_small(count, rows, cols):
     assert n <= max(1088 << 20, small), f"{n / 2 ** 20:.0f} MiB"
     # a single matrix of such rows fits as ever
     assert moe.moe_orthogonalize_workspace_size(1, rows, cols) <= 320 << 20
+
+
+@pytest.mark.parametrize("name", ["out", "momentum"])
+@pytest.mark.parametrize("shape", [(2, 40, 24), (24, 2, 40), (2, 960), (1920,), (3, 24, 40)])
+def test_orthogonalize_refuses_other_shapes(name, shape):
+    """As many values in another order, which would be filled as if they were grad's, or more."""
+    torch = pytest.importorskip("torch")
+    a = calls(torch)["moe_orthogonalize"]
+    a[name] = a[name].new_zeros(shape)
+    with pytest.raises(ValueError, match=name):
+        moe.moe_orthogonalize(**a, stream=0)
+
+
+def test_orthogonalize_takes_a_batch_of_one_either_way():
+    torch = pytest.importorskip("torch")
+    g = torch.zeros(24, 40)
+    with pytest.raises(ValueError, match="GPU"):  # past the shapes, to the next check
+        moe.moe_orthogonalize(g, g[None].bfloat16(), momentum=g[None].clone(), stream=0)
