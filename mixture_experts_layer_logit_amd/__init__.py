@@ -552,9 +552,19 @@ def _mx_fits(codes, scales):
     return True
 
 
+def _gpu_of(stream):
+    """The GPU that a call on this stream runs on: the current one without a stream and on
+    the null stream, a Stream's own; None for another handle, whose GPU is not known here."""
+    if stream is None or (isinstance(stream, int) and stream == 0):
+        if _device is None:
+            _fill_packed()
+        return _device()
+    return getattr(stream, "device_index", None)
+
+
 def _on_gpu(stream, tensors):
-    """ValueError for a tensor that is not on the GPU the call runs on: the current
-    one, or any single one where a stream is given.  None and plain addresses pass."""
+    """ValueError for a tensor that is not on the GPU the call runs on, or, where that is
+    not known, not on the first one's.  None and plain addresses pass."""
     at = None
     for t in tensors:
         if t is None or isinstance(t, int):
@@ -564,12 +574,9 @@ def _on_gpu(stream, tensors):
             if here < 0:
                 raise ValueError(f"a tensor of shape {tuple(t.shape)} is not on a GPU")
             if at is None:
-                at = here
-                if stream is not None:
-                    continue
-                if _device is None:
-                    _fill_packed()
-                at = _device()
+                at = _gpu_of(stream)
+                if at is None:
+                    at = here
                 if here == at:
                     continue
             raise ValueError(f"a tensor of shape {tuple(t.shape)} is on GPU {here}, not on GPU {at}")
@@ -581,7 +588,7 @@ def _quantised_rows(wide, name, codes, scales, stream):
         dt, n, at = _src_types[wide.dtype], wide.numel(), wide.get_device()
         fits = (codes.dtype in _packed and _scale_types.get(scales.dtype) == MOE_SCALE_E8M0 and 2 * codes.numel() >= n
                 and 32 * scales.numel() >= n and at == codes.get_device() == scales.get_device() >= 0
-                and (stream is not None or at == _device()))
+                and (at == _device() if stream is None else _gpu_of(stream) in (None, at)))
     except (AttributeError, KeyError, TypeError):  # among them a process's first call
         fits = False
     if not fits:

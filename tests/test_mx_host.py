@@ -326,3 +326,32 @@ def test_orthogonalize_takes_a_batch_of_one_either_way():
     g = torch.zeros(24, 40)
     with pytest.raises(ValueError, match="GPU"):  # past the shapes, to the next check
         moe.moe_orthogonalize(g, g[None].bfloat16(), momentum=g[None].clone(), stream=0)
+
+
+class Handle:
+    """A stream of GPU 0."""
+    device_index, cuda_stream = 0, 0x1000
+
+
+@pytest.mark.parametrize("fn", list(calls(pytest.importorskip("torch"))))
+@pytest.mark.parametrize("stream", [None, 0, Handle()], ids=["none", "null", "stream"])
+def test_bindings_refuse_tensors_of_another_gpu(fn, stream, monkeypatch):
+    """The current GPU is 0, the tensors are on GPU 1: without a stream, on the null stream and on
+    a stream of GPU 0 the kernels would run on GPU 0 and read addresses of GPU 1."""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu1(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def place(v):
+        return {n: place(t) for n, t in v.items()} if isinstance(v, dict) else v.as_subclass(OnGpu1) if torch.is_tensor(v) else v
+
+    moe._fill_packed()
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    monkeypatch.setattr(moe, "load", lambda: pytest.fail("reached the library"))
+    a = place(calls(torch)[fn])
+    with pytest.raises(ValueError, match="on GPU 1, not on GPU 0"):
+        getattr(moe, fn)(**a, stream=stream)
+    # a bare handle's GPU is not known: the tensors have to agree with each other
+    moe._on_gpu(0x1000, [t for t in a.values() if torch.is_tensor(t)])
