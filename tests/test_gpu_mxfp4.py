@@ -642,3 +642,67 @@ def test_weights_of_more_than_4_gib(roomy):
         v, dv = ref.product(h[r], picked("down", e))
         over = np.abs(y[r].double().cpu().numpy()[:, rows_of["down"]] - v) - (dv + ref.U8 * (np.abs(v) + dv))
         assert np.all(over <= 0), f"down, expert {e}"
+
+
+# ---------------------------------------------------------------- malformed segments write nothing else
+class Guarded:
+    """A tensor in the middle of a larger one of a known pattern."""
+    EDGE = 1 << 16
+
+    def __init__(self, *shape, dtype=torch.uint8):
+        n = int(np.prod(shape))
+        size = torch.empty(0, dtype=dtype).element_size()
+        self.all = torch.full((n * size + 2 * self.EDGE,), 0x5A, dtype=torch.uint8, device="cuda")
+        self.mid = self.all[self.EDGE:self.EDGE + n * size]
+        self.t = self.mid.view(dtype).view(*shape)
+
+    def edges_stay(self):
+        return bool(torch.all(self.all[:self.EDGE] == 0x5A)) and bool(torch.all(self.all[self.EDGE + self.mid.numel():] == 0x5A))
+
+    def rows(self):
+        """Rows as bytes."""
+        return self.mid.view(self.t.shape[0], -1).cpu().numpy()
+
+
+def clamped_rows(off, rows):
+    """The rows of every segment, its borders clamped into [0, rows] and its end not in front of its start."""
+    held = np.zeros(rows, bool)
+    for e in range(len(off) - 1):
+        lo = min(max(int(off[e]), 0), rows)
+        held[lo:min(max(int(off[e + 1]), lo), rows)] = True
+    return held
+
+
+@pytest.mark.parametrize("shape", [(40, 256, 4, 1, 256, "relu"), (40, 256, 4, 1, 384, "swiglu"), (300, 5632, 4, 2, 384, "relu"),
+                                   (700, 256, 4, 1, 2304, "swiglu")], ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("off", [[0, 1 << 30, -5, 60, 40], [-7, 3, 3, 1 << 30, -(1 << 30)], [11, 5, 17, 17, 23], [-1, -1, -1, -1, -1],
+                                 [1 << 30, 1 << 30, 1 << 30, 1 << 30, 1 << 30]], ids=lambda o: "_".join(map(str, o)))
+@pytest.mark.parametrize("ws", [False, True])
+def test_malformed_segments_write_their_clamped_rows_only(shape, off, ws):
+    """Tokens and segments that no routing gives: outputs and workspace lie between guards, rows
+    outside every clamped segment keep what they held, and a row of one valid segment and a
+    valid token is as in a call without the others."""
+    print(f"[mxfp4 malformed] {shape} {off} {ws}", flush=True)
+    T, d, E, k, F, act = shape
+    c = Case(T, d, E, k, F, act, "even")
+    rows = T * k
+    src = c.src.copy()
+    src[::7], src[3], src[5] = 1 << 29, -1, T
+    off = np.array(off, np.int32)
+    hq, hs, y = Guarded(rows, F // 2), Guarded(rows, F // BLK), Guarded(rows, d, dtype=torch.bfloat16)
+    space = Guarded(moe.moe_mxfp4_workspace_size(c.p)) if ws else None
+    moe.moe_expert_up_mxfp4(c.p, dev(c.xq), dev(c.xs), dev(src), dev(off), dev(c.W1), dev(c.s1), hq.t, hs.t, ws=space and space.t)
+    moe.moe_expert_down_mxfp4(c.p, dev(c.hq), dev(c.hs), dev(off), dev(c.W2), dev(c.s2), y.t, ws=space and space.t)
+    torch.cuda.synchronize()
+    held = clamped_rows(off, rows)
+    for name, g in dict(hq=hq, hs=hs, y=y).items():
+        assert g.edges_stay(), f"{name}: written outside"
+        assert np.all(g.rows()[~held] == 0x5A), f"{name}: a row outside every segment"
+    assert space is None or space.edges_stay(), "workspace: written outside"
+    # [11, 5, 17, 17, 23]: 5 .. 16 of expert 1 and 17 .. 22 of expert 3 are segments like any
+    if list(off) == [11, 5, 17, 17, 23]:
+        c.off = np.array([5, 5, 17, 17, 23], np.int32)
+        good = (src >= 0) & (src < T) & held
+        want_q, want_s = c.up(ws=c.workspace(0) if ws else None)
+        assert np.array_equal(hq.rows()[good], want_q[good]) and np.array_equal(hs.rows()[good], want_s[good])
+        c.check_down(y.t.double().cpu().numpy())
