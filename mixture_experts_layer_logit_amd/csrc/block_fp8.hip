@@ -207,8 +207,10 @@ __device__ __forceinline__ int block_parts(int total, int G, int nk, bool enable
     return max(1, min(min(kBlkMaxParts, min(G, kBlkSplitSlots) / tail), nk / kBlkMinPart));
 }
 
-// silu(u) v, silu(u) = u / (1 + e^-u); the exponential and the reciprocal to
-// within a step or two of fp32, which the E4M3 code behind them does not see.
+// silu(u) v, silu(u) = u / (1 + e^-u), off by (1.3 |u| + 8) 2^-24 of the result where u
+// is negative (the exponent is rounded to fp32), by 8 of 2^-24 where it is positive; 0 below
+// about -87, where e^-u leaves fp32's range.  A value or a block's maximum that lies
+// this close to a border can take the code on its other side.
 __device__ __forceinline__ float glu(float u, float v)
 {
     return u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) * v;

@@ -128,8 +128,11 @@ __device__ __forceinline__ int mx_parts(int total, int G, int nk, bool enabled)
     return max(1, min(min(kMxMaxParts, min(G, kMxSplitSlots) / tail), nk / kMxMinPart));
 }
 
-// silu(u) v, silu(u) = u / (1 + e^-u); the exponential and the reciprocal to within a
-// step or two of fp32, which the E2M1 code behind them does not see.
+// silu(u) v, silu(u) = u / (1 + e^-u).  The exponent is rounded to fp32, which costs
+// the exponential |u| 1.3 of 2^-24, and it and the reciprocal are a step or so off
+// themselves: (1.3 |u| + 8) 2^-24 of the result where u is negative, 8 of 2^-24 where it is
+// positive; below about -87, where e^-u leaves fp32's range, the result is 0.  A value or
+// a block's maximum that lies this close to a border can take the code on its other side.
 __device__ __forceinline__ float mx_glu(float u, float v)
 {
     return u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f)) * v;

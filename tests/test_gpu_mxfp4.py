@@ -706,3 +706,30 @@ def test_malformed_segments_write_their_clamped_rows_only(shape, off, ws):
         want_q, want_s = c.up(ws=c.workspace(0) if ws else None)
         assert np.array_equal(hq.rows()[good], want_q[good]) and np.array_equal(hs.rows()[good], want_s[good])
         c.check_down(y.t.double().cpu().numpy())
+
+
+def test_negative_gates():
+    """silu of gates down to -87 within (1.3 |u| + 8) 2^-24 of it: the exponent's rounding grows with
+    |u|.  A gate is the sum of two codes whose scales lie at most 2^6 apart and an up value one
+    code, so both are exact."""
+    T, d, F = 400, 128, 128
+    g = gen(41)
+    p = moe.problem(T, d, 1, 1, F, act="swiglu")
+    codes, e = np.zeros((T, d), np.uint8), np.zeros((T, d // BLK), np.int64)
+    e[:, 0] = g.integers(-4, 4, T)
+    e[:, 1] = e[:, 0] - g.integers(0, 4, T)
+    codes[:, 0], codes[:, 32], codes[:, 64] = g.integers(1, 8, T), g.integers(0, 8, T), 2
+    W, we = np.zeros((1, 2 * F, d), np.uint8), np.zeros((1, 2 * F, d // BLK), np.int64)
+    W[0, :F, 0] = W[0, :F, 32] = 10  # -1
+    W[0, F:, 64] = g.integers(0, 16, F)
+    u = -(ref.POS[codes[:, 0]] * np.exp2(e[:, 0]) + ref.POS[codes[:, 32]] * np.exp2(e[:, 1]))
+    keep = u > -87
+    assert np.count_nonzero(keep) > 300 and u[keep].min() < -60
+    h = (u / (1 + np.exp(-u)))[:, None] * ref.TABLE[W[0, F:, 64]][None, :]
+    hq = torch.empty(T, F // 2, dtype=torch.uint8, device="cuda")
+    hs = torch.empty(T, F // BLK, dtype=torch.uint8, device="cuda")
+    moe.moe_expert_up_mxfp4(p, dev(ref.pack(codes)), dev((e + 127).astype(np.uint8)), None, dev(np.array([0, T], np.int32)), dev(ref.pack(W)),
+                            dev((we + 127).astype(np.uint8)), hq, hs)
+    torch.cuda.synchronize()
+    dh = (1.3 * np.abs(u) + 8)[:, None] * ref.U24 * np.abs(h)
+    ref.check_quantised(hq.cpu().numpy()[keep], hs.cpu().numpy()[keep].astype(np.int64) - 127, h[keep], dh[keep], "negative gates")
