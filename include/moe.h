@@ -566,17 +566,18 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  * fp64, in a fixed order.  The same bits on every run.  A matrix whose U
  * holds a NaN or an infinity becomes NaN as a whole and leaves the others alone.
  * Error against the 64-bit result, in the norm of that result, before out's own
- * rounding.  Up to 64 rows (or columns) and 7 steps: fp64 steps and one fp32 product, at
- * most 1e-4 up to 5 steps and 1e-3 at 7.  Else the products run on fp16 operands
- * with fp32 sums, scaled so that no range is lost.  The quintic's slope, up to 3.97,
- * carries each step's roundings on through the next, so the error goes by the matrix and the
- * steps and has no bound that serves them all.  The largest seen:
+ * rounding.  Up to 64 rows (or columns) and 7 steps the steps run in fp64 and the last
+ * product in fp32.  Else the products run on fp16 operands with fp32 sums, scaled so
+ * that no range is lost.  The quintic's slope, up to 3.97, carries each step's roundings
+ * on through the next, so the error goes by the matrix and the steps and has no bound
+ * that serves them all.  The largest seen:
  *   steps                                                      1-5      6-8      9-64
  *   full rank, singular values that differ (Gaussian
  *   gradients, sums over more tokens than rows)                1.5e-3   4e-3     2e-2
  *   equal singular values: orthonormal or repeated rows,
  *   blocks of equal entries                                    1.2e-2   3e-2     0.12
  *   singular values of zero (fewer tokens than rows)           1.5e-3   2.5e-3   -
+ *   up to 64 rows and 7 steps, all of these                    1e-4     1e-3
  * What a rounding leaves in the direction of a singular value next to zero grows by 3.44 a
  * step, in this as in any arithmetic: here it is 2e-2 of the result at 10 steps and 0.2 at
  * 12, and behind those these directions are as large as the rest.
